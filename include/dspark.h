@@ -334,6 +334,76 @@ DSPARK_API dspark_status_t dspark_tp_heads_bwd(const dspark_problem_t* prob, con
                                                const dspark_grads_t* grads, void* ws, size_t ws_bytes,
                                                dspark_stream_t stream);
 
+/*
+ * Linear cross entropy: the cross entropy of the logits z = hidden . weight^T of R rows
+ * over the whole vocabulary, from the hidden rows and the head, with its gradients.  The
+ * logits are never kept: the forward leaves one logsumexp per row, the backward forms
+ * dL/dz again, one piece of the vocabulary at a time.  (The CE term of dspark_loss_fwd,
+ * for callers that have hidden rows instead of logits.)
+ *   lse_r = logsumexp(z_r),   CE_r = lse_r - z_r[target_r]
+ *   loss  = sum_r w_r * (CE_r + z_alpha * lse_r^2)          (unnormalised numerator)
+ *   dz_r  = g * w_r * (softmax(z_r) * (1 + 2 z_alpha lse_r) - onehot(target_r))
+ *   dhidden_r = weight^T dz_r,   dweight = sum_r dz_r (x) hidden_r
+ * A row whose target is ignore_index has no label: it contributes nothing, its outputs and
+ * its dhidden row are zero, and its hidden values are not read.  A target that is neither
+ * ignore_index nor in [0, V) raises DSPARK_ERR_ID_OUT_OF_RANGE and counts as no label.
+ *
+ * hidden and weight are bf16, products are accumulated in FP32; logits, logsumexps and
+ * losses are FP32, the loss sum FP64.  dL/dz is rounded once to bf16 before the two
+ * gradient products (they run on the bf16 tensor cores), whose FP32 sums are rounded once
+ * to the output type.  Two runs give the same bits.
+ * H, the leading dimensions and every matrix pointer obey the 16-byte rule above; V and R
+ * are free.  Sizes above 2^30 columns, 2^24 rows, a hidden size above 2^20 or more than
+ * 2^31 - 1 tiles (R/128 x V/128) are DSPARK_ERR_UNSUPPORTED.
+ */
+typedef struct {
+  int64_t R, V, H;             /* rows, vocabulary, hidden size (a multiple of 8)       */
+  const void* hidden;          /* bf16 [R, H], row stride hidden_ld elements            */
+  int64_t hidden_ld;
+  const void* weight;          /* bf16 [V, H] (the head), row stride weight_ld          */
+  int64_t weight_ld;
+  const int64_t* targets;      /* [R] label in [0, V), or ignore_index                  */
+  int64_t ignore_index;        /* e.g. -100; wins where it lies in [0, V)               */
+  const float* row_weight;     /* [R] w_r, or NULL = 1                                  */
+  float z_alpha;               /* weight of lse^2; 0 = plain cross entropy              */
+} dspark_lce_problem_t;
+
+/* Forward outputs; each may be NULL. */
+typedef struct {
+  float* loss_num;             /* [1] unnormalised weighted numerator                   */
+  int64_t* num_tokens;         /* [1] labelled rows (exact)                             */
+  float* ce_rows;              /* [R] CE per row, 0 without a label                     */
+  float* lse_rows;             /* [R] logsumexp per row, 0 without a label              */
+} dspark_lce_out_t;
+
+/* Gradients; dhidden and dweight may each be NULL (a frozen head, a frozen drafter). */
+typedef struct {
+  const float* grad_scale;     /* device scalar g = d(objective)/d(loss_num); NULL = 1  */
+  void* dhidden;               /* bf16 [R, H], written for every row                    */
+  int64_t dhidden_ld;
+  void* dweight;               /* [V, H], row stride dweight_ld                         */
+  int64_t dweight_ld;
+  int64_t dweight_dtype;       /* dspark_dtype_t: DSPARK_BF16 or DSPARK_F32             */
+  int64_t accumulate;          /* 1: dweight += (DSPARK_F32 only); 0: overwritten       */
+} dspark_lce_grads_t;
+
+/* Bytes of device workspace for `prob`: for the forward alone (grads NULL), or for the
+ * forward and the backward with these gradients.  0 on an invalid problem.  Depends on the
+ * sizes and on which gradients are non-NULL.  With gradients it holds a piece of dL/dz of
+ * about 256 MiB at most (never less than 256 columns of it). */
+DSPARK_API size_t dspark_lce_workspace_size(const dspark_lce_problem_t* prob, const dspark_lce_grads_t* grads);
+
+/* Forward.  `ws` 256-byte aligned, dspark_lce_workspace_size(prob, NULL) bytes, or as many
+ * as the backward needs if one follows on the same workspace. */
+DSPARK_API dspark_status_t dspark_lce_fwd(const dspark_lce_problem_t* prob, const dspark_lce_out_t* out, void* ws,
+                                          size_t ws_bytes, dspark_stream_t stream);
+
+/* Backward of the dspark_lce_fwd that last ran on `ws`, with the same problem: reads the
+ * row list, the labelled hidden rows and the logsumexps it left there, and weight again.
+ * May be called more than once after one forward. */
+DSPARK_API dspark_status_t dspark_lce_bwd(const dspark_lce_problem_t* prob, const dspark_lce_grads_t* grads, void* ws,
+                                          size_t ws_bytes, dspark_stream_t stream);
+
 /* Synchronises `stream` and returns the first device-side error recorded in `ws`
  * by the last call that used it (DSPARK_OK if none). */
 DSPARK_API dspark_status_t dspark_check_status(const void* ws, dspark_stream_t stream);

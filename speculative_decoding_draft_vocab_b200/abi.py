@@ -89,6 +89,29 @@ class dspark_tp_t(ctypes.Structure):
     _fields_ = [("tp_size", c_i64), ("vocab_begin", c_i64), ("vocab_size", c_i64)]
 
 
+class dspark_lce_problem_t(ctypes.Structure):
+    _fields_ = [
+        ("R", c_i64), ("V", c_i64), ("H", c_i64),
+        ("hidden", c_vp), ("hidden_ld", c_i64),
+        ("weight", c_vp), ("weight_ld", c_i64),
+        ("targets", c_vp), ("ignore_index", c_i64),
+        ("row_weight", c_vp), ("z_alpha", ctypes.c_float),
+    ]
+
+
+class dspark_lce_out_t(ctypes.Structure):
+    _fields_ = [("loss_num", c_vp), ("num_tokens", c_vp), ("ce_rows", c_vp), ("lse_rows", c_vp)]
+
+
+class dspark_lce_grads_t(ctypes.Structure):
+    _fields_ = [
+        ("grad_scale", c_vp),
+        ("dhidden", c_vp), ("dhidden_ld", c_i64),
+        ("dweight", c_vp), ("dweight_ld", c_i64), ("dweight_dtype", c_i64),
+        ("accumulate", c_i64),
+    ]
+
+
 # floats per row of the two exchange records of the vocabulary-parallel path
 DSPARK_TP_REC1_FLOATS = 8
 DSPARK_TP_REC2_FLOATS = 4
@@ -119,6 +142,12 @@ lib.dspark_tp_finish.restype = ctypes.c_int
 lib.dspark_tp_heads_bwd.argtypes = [P(dspark_problem_t), P(dspark_params_t), P(dspark_tp_t), c_vp,
                                     P(dspark_grads_t), c_vp, ctypes.c_size_t, c_vp]
 lib.dspark_tp_heads_bwd.restype = ctypes.c_int
+lib.dspark_lce_workspace_size.argtypes = [P(dspark_lce_problem_t), P(dspark_lce_grads_t)]
+lib.dspark_lce_workspace_size.restype = ctypes.c_size_t
+lib.dspark_lce_fwd.argtypes = [P(dspark_lce_problem_t), P(dspark_lce_out_t), c_vp, ctypes.c_size_t, c_vp]
+lib.dspark_lce_fwd.restype = ctypes.c_int
+lib.dspark_lce_bwd.argtypes = [P(dspark_lce_problem_t), P(dspark_lce_grads_t), c_vp, ctypes.c_size_t, c_vp]
+lib.dspark_lce_bwd.restype = ctypes.c_int
 lib.dspark_check_status.argtypes = [c_vp, c_vp]
 lib.dspark_check_status.restype = ctypes.c_int
 lib.dspark_status_string.argtypes = [ctypes.c_int]
@@ -140,6 +169,9 @@ dspark_tp_partials = lib.dspark_tp_partials
 dspark_tp_l1 = lib.dspark_tp_l1
 dspark_tp_finish = lib.dspark_tp_finish
 dspark_tp_heads_bwd = lib.dspark_tp_heads_bwd
+dspark_lce_workspace_size = lib.dspark_lce_workspace_size
+dspark_lce_fwd = lib.dspark_lce_fwd
+dspark_lce_bwd = lib.dspark_lce_bwd
 dspark_check_status = lib.dspark_check_status
 dspark_status_string = lib.dspark_status_string
 dspark_last_cuda_error = lib.dspark_last_cuda_error

@@ -11,6 +11,15 @@
 
 using namespace dspark;
 
+// The CUDA error behind the most recent DSPARK_ERR_CUDA of any call in this process.
+static std::atomic<int> g_last_cuda_error{0};
+
+dspark_status_t dspark::cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return DSPARK_OK;
+  g_last_cuda_error.store(int(e), std::memory_order_relaxed);
+  return DSPARK_ERR_CUDA;
+}
+
 namespace {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -120,15 +129,6 @@ dspark_status_t check_problem(const dspark_problem_t* p, const dspark_params_t* 
   if (sweep && !sweep_supported(sweep_kind(p), p->V, s.has_teacher)) return DSPARK_ERR_UNSUPPORTED;
   *sh = s;
   return DSPARK_OK;
-}
-
-// The CUDA error behind the most recent DSPARK_ERR_CUDA of any call in this process.
-std::atomic<int> g_last_cuda_error{0};
-
-inline dspark_status_t cuda_status(cudaError_t e) {
-  if (e == cudaSuccess) return DSPARK_OK;
-  g_last_cuda_error.store(int(e), std::memory_order_relaxed);
-  return DSPARK_ERR_CUDA;
 }
 
 dspark_status_t check_ws(const dspark_problem_t* p, const void* ws, size_t ws_bytes) {

@@ -5,6 +5,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "dspark.h"
 
 namespace dspark {
@@ -260,6 +262,9 @@ constexpr int heads_splits(int64_t R, int64_t V) {
   const int64_t s = kHeadsSlots / m_tiles;
   return int(s < 1 ? 1 : (s > kchunks ? kchunks : s));
 }
+
+// DSPARK_OK, or DSPARK_ERR_CUDA with the error kept for dspark_last_cuda_error().
+dspark_status_t cuda_status(cudaError_t e);
 
 // ------------------------------------------------------------------ launchers
 cudaError_t launch_prologue(const PrologueArgs& a, cudaStream_t s);

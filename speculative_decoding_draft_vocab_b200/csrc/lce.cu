@@ -1,0 +1,841 @@
+// Linear cross entropy: softmax cross entropy of z = hidden . weight^T over the whole
+// vocabulary and its gradients, the logits never kept.
+//   forward   prep:  the labelled rows' list, their hidden rows gathered compact
+//             fwd:   product tiles; each row's (maximum, sum of exponentials) in the tile
+//             merge: logsumexp, CE and the loss from the tiles' pairs
+//   backward, a piece of the vocabulary at a time:
+//             dz:    the product again; dL/dz of the piece, bf16
+//             dw:    dweight rows of the piece = dz^T . hidden
+//             dh:    partial sums of dhidden = dz . weight, FP32
+//             then dhidden from the partial sums, scattered to the labelled rows
+// A label's row appears in no product unless it is labelled (ignore_index rows are neither
+// read nor computed), so masked batches pay for their labels only.
+//
+// The four products share one kernel: tcgen05.mma (bf16 in, FP32 in TMEM), fed by TMA.
+// CG CTAs (one, or a cluster of two sharing a 256-row tile through cta_group::2) form a
+// tile; 320 threads each:
+//   warp 0      one thread issues the TMA loads into a ring of 64-wide K stages
+//   warp 1      allocates TMEM; one thread (of the tile's first CTA) issues the MMAs
+//   warps 2..9  read the accumulator (a thread: one tile row, half the columns), finish it
+// The accumulator is double-buffered in TMEM: a tile's epilogue runs beside the next
+// tile's MMAs.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "lce.cuh"
+#include "tc_host.cuh"
+
+namespace dspark {
+namespace lce {
+namespace {
+
+using tc::BK;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;"); }
+
+// ------------------------------------------------------------------ prep
+// Each CTA takes a contiguous run of rows, counts the labelled rows before it (the labels
+// are small and in L2) and writes its part of the list; then its warps copy the labelled
+// hidden rows.  The last CTA, which sees every row, writes the counts and the status and
+// zero-fills the compact rows up to a whole 64-row K chunk: the dweight product reads
+// those, and zero is what they have to add.
+constexpr int kPrepThreads = 256;
+
+__global__ void __launch_bounds__(kPrepThreads) prep_kernel(const dspark_lce_problem_t p, const View ws,
+                                                            int64_t* num_tokens, int64_t rows_per_cta) {
+  pdl_trigger();
+  __shared__ int sh_warp[kPrepThreads / 32];
+  __shared__ int sh_before, sh_bad, sh_pos[kPrepThreads];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t r0 = int64_t(blockIdx.x) * rows_per_cta;
+  const int64_t r1 = r0 + rows_per_cta < p.R ? r0 + rows_per_cta : p.R;
+  const bool last = blockIdx.x == gridDim.x - 1;
+  if (tid == 0) sh_before = 0, sh_bad = 0;
+  __syncthreads();
+  // labelled rows before r0 (and, in the last CTA, any label out of range)
+  int n = 0, bad = 0;
+  for (int64_t r = tid; r < (last ? r1 : r0); r += kPrepThreads) {
+    const int64_t t = p.targets[r];
+    const bool in = t >= 0 && t < p.V;
+    if (t != p.ignore_index) {
+      if (!in) bad = 1;
+      else if (r < r0) ++n;
+    }
+  }
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0) atomicAdd(&sh_before, n);
+  if (bad) sh_bad = 1;
+  __syncthreads();
+  int base = sh_before;
+  for (int64_t c0 = r0; c0 < r1; c0 += kPrepThreads) {
+    const int64_t r = c0 + tid;
+    int64_t t = -1;
+    bool live = false;
+    if (r < r1) {
+      t = p.targets[r];
+      live = t != p.ignore_index && t >= 0 && t < p.V;
+    }
+    const uint32_t mask = __ballot_sync(0xffffffffu, live);
+    if (lane == 0) sh_warp[warp] = __popc(mask);
+    __syncthreads();
+    int at = base + __popc(mask & ((1u << lane) - 1u));
+    int total = 0;
+    for (int w = 0; w < kPrepThreads / 32; ++w) {
+      if (w < warp) at += sh_warp[w];
+      total += sh_warp[w];
+    }
+    if (r < r1) ws.index[r] = live ? at : -1;
+    if (live) {
+      ws.list[at] = int32_t(r);
+      ws.tok[at] = int32_t(t);
+      ws.w[at] = p.row_weight ? p.row_weight[r] : 1.f;
+    }
+    sh_pos[tid] = live ? at : -1;
+    __syncthreads();
+    // the labelled rows of this run: one warp per row
+    for (int k = warp; k < kPrepThreads && c0 + k < r1; k += kPrepThreads / 32) {
+      const int pos = sh_pos[k];
+      if (pos < 0) continue;  // the whole warp
+      const uint4* src =
+          reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.hidden) + size_t(c0 + k) * p.hidden_ld);
+      uint4* dst = reinterpret_cast<uint4*>(ws.hsup + size_t(pos) * p.H);
+#pragma unroll 4
+      for (int64_t j = lane; j < p.H / 8; j += 32) dst[j] = src[j];
+    }
+    __syncthreads();
+    base += total;
+  }
+  if (last) {
+    const int64_t pad = (int64_t(base) + 63) / 64 * 64;
+    uint4* z0 = reinterpret_cast<uint4*>(ws.hsup + size_t(base) * p.H);
+    const int64_t nz = (pad - base) * p.H / 8;
+    for (int64_t j = tid; j < nz; j += kPrepThreads) z0[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid == 0) {
+      ws.hdr->status = sh_bad ? kFlagIdOutOfRange : 0u;
+      ws.hdr->n_valid = base;
+      ws.hdr->done = 0;
+      if (num_tokens) *num_tokens = base;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ the products
+// Work item w -> (m tile, n tile, K split).  Items run through groups of `group` m tiles,
+// m fastest inside a group: the tiles in flight at one time share both operands in L2.
+struct Work {
+  int m_tiles, n_tiles, ksplit, kchunks, group;
+  int bound_m, bound_k;  // the number of labelled rows bounds the tile rows / the K range
+  const int32_t* n_valid;
+};
+
+struct Item {
+  int mt, nt, s, kc0, kc1;
+};
+
+__device__ __forceinline__ Item decode(const Work& wk, int w, int me, int kch) {
+  Item it;
+  const int per = me * wk.n_tiles;
+  it.s = w / per;
+  int t = w - it.s * per;
+  const int span = wk.group * wk.n_tiles;
+  const int g = t / span;
+  t -= g * span;
+  const int m0 = g * wk.group;
+  const int gm = min(wk.group, me - m0);
+  it.nt = t / gm;
+  it.mt = m0 + (t - it.nt * gm);
+  it.kc0 = int((int64_t(it.s) * kch) / wk.ksplit);
+  it.kc1 = int((int64_t(it.s + 1) * kch) / wk.ksplit);
+  return it;
+}
+
+enum : int { kFwd = 0, kDz = 1, kDh = 2, kDwBf16 = 3, kDwF32 = 4 };
+
+struct EpiArgs {
+  View ws;
+  int64_t Rp;
+  int32_t rows, n_cols;      // rows and columns of the product that exist
+  int32_t col0;              // first vocabulary id of the piece
+  float z_alpha;
+  const float* grad_scale;
+  int32_t add;               // dh: add to the planes; dw: add to dweight
+};
+
+template <int CG>
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
+  if constexpr (CG == 1) {
+    return mbar_wait_bounded(bar, parity);
+  } else {
+    // arrivals may come from the other CTA of the pair: acquire at cluster scope
+    auto test = [&]() {
+      uint32_t done;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+      return done != 0;
+    };
+    if (test()) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+      for (int i = 0; i < 64; ++i)
+        if (test()) return true;
+      if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+    }
+  }
+}
+
+// TMA tile load completing on the barrier of the tile's first CTA.
+template <int CG>
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if constexpr (CG == 1) {
+    tc::tma_load_2d(dst, map, x, y, bar);
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+  }
+}
+
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (CG == 1) {
+    tc::mma_bf16(d, a, b, idesc, acc);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+  }
+}
+
+// Arrive on `bar` (in every CTA of the tile) once this thread's MMAs so far are done.
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (CG == 1) {
+    tc::mma_commit(bar);
+  } else {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(bar), "h"(uint16_t(3)) : "memory");
+  }
+}
+
+__device__ __forceinline__ void reduce_add_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%1, %2, %3}], [%4];"
+               ::"l"(map), "r"(x), "r"(y), "r"(z), "r"(src) : "memory");
+}
+
+__device__ __forceinline__ void st_shared_u4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// 16 consecutive fp32 columns of this thread's TMEM lane (warp-collective).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
+                 "+f"(v[15])::"memory");
+}
+
+template <int CG>
+constexpr uint32_t stage_bytes() { return uint32_t(kBM * BK * 2 + 256 / CG * BK * 2); }
+template <int CG>
+constexpr int stages() { return CG == 1 ? 4 : 6; }
+template <int CG>
+constexpr size_t smem_bytes() { return size_t(stages<CG>()) * stage_bytes<CG>() + 1024 + kEpiWarps * 4096 + 1024; }
+
+// One epilogue warp's share of a tile: 32 rows (row = this thread's lane, `m0 + lane`) and the
+// columns [c0, c1) of the tile, at TMEM address `taddr` + column.  `n0`: first product
+// column of the tile.
+struct Share {
+  uint32_t taddr;
+  uint32_t sbuf;   // this warp's 4 KB staging tile
+  int m0, n0, c0, c1;
+  int nt, half, split;
+  bool empty;      // no K range: the product is zero and the accumulator was not written
+  int n_valid, lane;
+};
+
+// The staging tile may be written again once the TMA engine has read it.
+__device__ __forceinline__ void staging_free(int lane) {
+  if (lane == 0) tc::bulk_wait_read<0>();
+  __syncwarp();
+}
+
+// 32 rows x 128 bytes, 16-byte chunk k of row `lane` at chunk k ^ (lane % 8): the 128-byte swizzle
+__device__ __forceinline__ void stage_row(uint32_t sbuf, int lane, const uint32_t* o) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    st_shared_u4(sbuf + uint32_t(lane) * 128u + uint32_t((k ^ (lane & 7)) * 16), o[4 * k], o[4 * k + 1], o[4 * k + 2],
+                 o[4 * k + 3]);
+  tc::fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// Forward: (maximum, sum) of the row's exponentials over this share, base 2, and the logit
+// at the label, from the row's logits in registers.
+__device__ __forceinline__ void fwd_finish(const EpiArgs& a, const Share& sh, const float (&z)[128]) {
+  const int row = sh.m0 + sh.lane;
+  const int tgt = row < sh.n_valid ? a.ws.tok[row] - sh.n0 - sh.c0 : -1;
+  const int cols = min(sh.c1, a.n_cols - sh.n0) - sh.c0;  // <= 0: wholly past the vocabulary
+  float zt = 0.f;
+  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if (uint32_t(tgt - 32 * c) < 32u && tgt < cols) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) zt = tgt - 32 * c == i ? z[32 * c + i] : zt;
+      a.ws.zt[row] = zt;
+    }
+    if (cols - 32 * c >= 32) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], z[32 * c + i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (32 * c + i < cols) m4[i & 3] = fmaxf(m4[i & 3], z[32 * c + i]);
+    }
+  }
+  const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * kLog2e;
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if (cols - 32 * c >= 32) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s4[i & 3] += ex2(fmaf(z[32 * c + i], kLog2e, -ref));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (32 * c + i < cols) s4[i & 3] += ex2(fmaf(z[32 * c + i], kLog2e, -ref));
+    }
+  }
+  if (row < sh.n_valid)
+    a.ws.part[size_t(2 * sh.nt + sh.half) * a.Rp + row] = make_float2(mx, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+}
+
+// dL/dz = w g (p (1 + 2 z_alpha lse) - onehot), rounded once to bf16; zero past the last
+// labelled row and past the vocabulary (those enter the gradient products).
+__device__ __forceinline__ void dz_finish(const EpiArgs& a, const CUtensorMap& out, const Share& sh) {
+  if (sh.m0 >= a.rows) return;  // the whole warp
+  const int row = sh.m0 + sh.lane;
+  const bool live = row < sh.n_valid;
+  const int tgt = live ? a.ws.tok[row] - a.col0 - sh.n0 : -1;
+  const float lse2 = live ? a.ws.lse2[row] : 0.f;
+  const float gw = live ? a.ws.w[row] * (a.grad_scale ? *a.grad_scale : 1.f) : 0.f;
+  const float scale = gw * fmaf(2.f * a.z_alpha, lse2 * kLn2, 1.f);
+  const int cols = live ? a.n_cols - sh.n0 : 0;
+#pragma unroll 1
+  for (int c = sh.c0; c < sh.c1; c += 64) {
+    uint32_t o[32];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[32];
+      __syncwarp();  // the TMEM load is warp-collective
+      tc::tmem_ld32(sh.taddr + uint32_t(c + 32 * h), v);
+      const int cc = c + 32 * h;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = ex2(fmaf(v[i], kLog2e, -lse2)) * scale;
+      if (uint32_t(tgt - cc) < 32u) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = tgt - cc == i ? v[i] - gw : v[i];
+      }
+      if (cols - cc < 32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = i < cols - cc ? v[i] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[16 * h + i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    }
+    staging_free(sh.lane);
+    stage_row(sh.sbuf, sh.lane, o);
+    if (sh.lane == 0) {
+      tc::tma_store_2d(&out, sh.sbuf, sh.n0 + c, sh.m0);
+      tc::bulk_commit();
+    }
+  }
+}
+
+// FP32 results: dhidden's partial sums (one plane per K split; a plane's element gets one
+// addition per piece, in stream order, so the sums have a fixed order), or dweight.
+template <bool PLANES>
+__device__ __forceinline__ void f32_finish(const EpiArgs& a, const CUtensorMap& out, const Share& sh) {
+  if (sh.m0 >= (PLANES ? sh.n_valid : a.rows) || (sh.empty && a.add)) return;
+#pragma unroll 1
+  for (int c = sh.c0; c < sh.c1 && sh.n0 + c < a.n_cols; c += 32) {
+    float v[32];
+    uint32_t o[32];
+    __syncwarp();
+    tc::tmem_ld32(sh.taddr + uint32_t(c), v);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = sh.empty ? 0u : __float_as_uint(v[i]);
+    staging_free(sh.lane);
+    stage_row(sh.sbuf, sh.lane, o);
+    if (sh.lane == 0) {
+      if constexpr (PLANES) {
+        if (a.add) reduce_add_3d(&out, sh.sbuf, sh.n0 + c, sh.m0, sh.split);
+        else tc::tma_store_3d(&out, sh.sbuf, sh.n0 + c, sh.m0, sh.split);
+      } else {
+        if (a.add) tc::tma_reduce_add_2d(&out, sh.sbuf, sh.n0 + c, sh.m0);
+        else tc::tma_store_2d(&out, sh.sbuf, sh.n0 + c, sh.m0);
+      }
+      tc::bulk_commit();
+    }
+  }
+}
+
+// dweight, rounded once to bf16
+__device__ __forceinline__ void bf16_finish(const EpiArgs& a, const CUtensorMap& out, const Share& sh) {
+  if (sh.m0 >= a.rows) return;
+#pragma unroll 1
+  for (int c = sh.c0; c < sh.c1 && sh.n0 + c < a.n_cols; c += 64) {
+    uint32_t o[32];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[32];
+      __syncwarp();
+      tc::tmem_ld32(sh.taddr + uint32_t(c + 32 * h), v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[16 * h + i] = sh.empty ? 0u : pack_bf16(v[2 * i], v[2 * i + 1]);
+    }
+    staging_free(sh.lane);
+    stage_row(sh.sbuf, sh.lane, o);
+    if (sh.lane == 0) {
+      tc::tma_store_2d(&out, sh.sbuf, sh.n0 + c, sh.m0);
+      tc::bulk_commit();
+    }
+  }
+}
+
+// Operand majors of each product: K-major = rows of 64 K values, MN-major = rows of 64
+// M (N) values per K index.  Boxes: K-major {64 K, rows}; MN-major {64 M/N, 64 K}.
+template <int CG, int EPI>
+__global__ void __launch_bounds__(kThreads, 1)
+product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const __grid_constant__ CUtensorMap tmO, const Work wk, const EpiArgs ea, const int bn) {
+  constexpr bool A_MN = EPI == kDwBf16 || EPI == kDwF32;
+  constexpr bool B_MN = EPI != kFwd && EPI != kDz;
+  constexpr int STAGES = stages<CG>();
+  // The tensor cores' FP32 accumulation rounds towards zero: over K = 4096 the logits come
+  // out 2.2e-6 short (relative), over K = 512 3e-7.  The forward hands over its accumulator
+  // every 512 values of K and the epilogue adds the segments in registers, rounding to
+  // nearest; the other products are rounded to bf16 right after, where it does not show.
+  constexpr int SEG = EPI == kFwd ? 512 / BK : 1 << 30;
+  constexpr uint32_t SA = kBM * BK * 2, SS = stage_bytes<CG>();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + size_t(STAGES) * SS);
+  const uint32_t full0 = smem_u32(bars);
+  const uint32_t empty0 = full0 + 8 * STAGES;
+  const uint32_t accf0 = empty0 + 8 * STAGES;
+  const uint32_t acce0 = accf0 + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 4);
+  uint8_t* stage = smem + size_t(STAGES) * SS + 1024;  // 1024-byte aligned
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = CG == 1 ? 0u : cluster_ctarank();
+  const int tile0 = int(blockIdx.x) / CG, tiles_step = int(gridDim.x) / CG;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accf0 + 8 * b, 1);
+      mbar_init(acce0 + 8 * b, kEpiWarps * CG);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    if constexpr (CG == 1) {
+      tc::tmem_alloc(smem_u32(tmem_slot), 512);
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;"
+                   ::"r"(smem_u32(tmem_slot)) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+  }
+  tc::fence_before_sync();
+  if constexpr (CG == 1) __syncthreads();
+  else cluster_sync();
+  tc::fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();  // what the kernel before it wrote
+  pdl_trigger();
+
+  const int n_valid = *wk.n_valid;
+  const int me = wk.bound_m ? min(wk.m_tiles, (n_valid + kBM * CG - 1) / (kBM * CG)) : wk.m_tiles;
+  const int kch = wk.bound_k ? min(wk.kchunks, (n_valid + BK - 1) / BK) : wk.kchunks;
+  const int W = me * wk.n_tiles * wk.ksplit;  // the same in every role
+  bool timed_out = false;
+
+  if (warp == 0 && lane == 0) {
+    // ---------------- TMA producer: this CTA's 128 rows of A, its 1/CG of B's columns
+    const int bnc = bn / CG;
+    const uint32_t tx = CG * (SA + uint32_t(bnc) * BK * 2);
+    int it = 0;
+    for (int w = tile0; w < W; w += tiles_step) {
+      const Item t = decode(wk, w, me, kch);
+      const int am = (t.mt * CG + int(rank)) * kBM, bn0 = t.nt * bn + int(rank) * bnc;
+      for (int kc = t.kc0; kc < t.kc1; ++kc, ++it) {
+        const int st = it % STAGES;
+        const uint32_t round = uint32_t(it / STAGES);
+        if (!wait_bar<CG>(empty0 + 8 * st, (round & 1u) ^ 1u)) timed_out = true;
+        uint32_t fb = full0 + 8 * st;
+        if (rank == 0) mbar_arrive_expect_tx(fb, tx);
+        else fb = dsmem_map(fb, 0);
+        const uint32_t sa = smem_u32(smem + size_t(st) * SS), sb = sa + SA;
+        const int k0 = kc * BK;
+        if constexpr (!A_MN) {
+          load_2d<CG>(sa, &tmA, k0, am, fb);
+        } else {
+#pragma unroll
+          for (int c = 0; c < kBM / 64; ++c) load_2d<CG>(sa + c * 8192, &tmA, am + c * 64, k0, fb);
+        }
+        if constexpr (!B_MN) {
+          load_2d<CG>(sb, &tmB, k0, bn0, fb);
+        } else {
+          for (int c = 0; c < bnc / 64; ++c) load_2d<CG>(sb + c * 8192, &tmB, bn0 + c * 64, k0, fb);
+        }
+      }
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ---------------- MMA issuer
+    const uint32_t idesc = tc::idesc_bf16(kBM * CG, bn, A_MN, B_MN);
+    int it = 0, tl = 0;
+    for (int w = tile0; w < W; w += tiles_step) {
+      const Item t = decode(wk, w, me, kch);
+      int kc = t.kc0;
+      do {  // one accumulator per segment (an empty K range still hands one over)
+        const int b = tl & 1;
+        if (!wait_bar<CG>(acce0 + 8 * b, (uint32_t(tl >> 1) & 1u) ^ 1u)) timed_out = true;
+        tc::fence_after_sync();
+        const uint32_t d_tmem = tmem_base + uint32_t(b * 256);
+        const int k1 = min(t.kc1, kc + SEG), kfirst = kc;
+        for (; kc < k1; ++kc, ++it) {
+          const int st = it % STAGES;
+          if (!wait_bar<CG>(full0 + 8 * st, uint32_t(it / STAGES) & 1u)) timed_out = true;
+          tc::fence_after_sync();
+          const uint32_t sa = smem_u32(smem + size_t(st) * SS), sb = sa + SA;
+#pragma unroll
+          for (int ks = 0; ks < BK / 16; ++ks) {
+            const uint64_t ad = A_MN ? tc::sdesc(sa + ks * 2048, 8192, 1024) : tc::sdesc(sa + ks * 32, 16, 1024);
+            const uint64_t bd = B_MN ? tc::sdesc(sb + ks * 2048, 8192, 1024) : tc::sdesc(sb + ks * 32, 16, 1024);
+            mma<CG>(d_tmem, ad, bd, idesc, (kc > kfirst || ks > 0) ? 1u : 0u);
+          }
+          commit<CG>(empty0 + 8 * st);  // frees the stage once these MMAs have read it
+        }
+        commit<CG>(accf0 + 8 * b);  // accumulator ready
+        ++tl;
+      } while (kc < t.kc1);
+    }
+  } else if (warp >= 2) {
+    // ---------------- epilogue: warp w reads TMEM lanes 32 * (w % 4) .. + 31 of its half
+    // of the columns
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t lanes = uint32_t(q * 32) << 16;
+    Share sh;
+    sh.sbuf = smem_u32(stage + (warp - 2) * 4096);
+    sh.half = half, sh.n_valid = n_valid, sh.lane = lane;
+    sh.c0 = half * (bn / 2), sh.c1 = sh.c0 + bn / 2;
+    auto release = [&](int b) {
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) tc::mbar_arrive(acce0 + 8 * b);
+        else asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                          ::"r"(dsmem_map(acce0 + 8 * b, 0)) : "memory");
+      }
+    };
+    int tl = 0;
+    for (int w = tile0; w < W; w += tiles_step) {
+      const Item t = decode(wk, w, me, kch);
+      sh.m0 = (t.mt * CG + int(rank)) * kBM + q * 32, sh.n0 = t.nt * bn;
+      sh.nt = t.nt, sh.split = t.s, sh.empty = t.kc0 == t.kc1;
+      if constexpr (EPI == kFwd) {
+        float z[128];
+#pragma unroll
+          for (int i = 0; i < 128; ++i) z[i] = 0.f;
+        for (int kc = t.kc0; kc < t.kc1; kc += SEG, ++tl) {
+          const int b = tl & 1;
+          if (!wait_bar<CG>(accf0 + 8 * b, uint32_t(tl >> 1) & 1u)) timed_out = true;
+          tc::fence_after_sync();
+          const uint32_t taddr = tmem_base + lanes + uint32_t(b * 256 + sh.c0);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            float v[16];
+            tmem_ld16(taddr + uint32_t(16 * c), v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z[16 * c + i] += v[i];
+          }
+          release(b);
+        }
+        fwd_finish(ea, sh, z);
+      } else {
+        const int b = tl & 1;
+        if (!wait_bar<CG>(accf0 + 8 * b, uint32_t(tl >> 1) & 1u)) timed_out = true;
+        tc::fence_after_sync();
+        sh.taddr = tmem_base + lanes + uint32_t(b * 256);
+        if constexpr (EPI == kDz) dz_finish(ea, tmO, sh);
+        else if constexpr (EPI == kDh) f32_finish<true>(ea, tmO, sh);
+        else if constexpr (EPI == kDwF32) f32_finish<false>(ea, tmO, sh);
+        else bf16_finish(ea, tmO, sh);
+        release(b);
+        ++tl;
+      }
+    }
+    if (lane == 0) tc::bulk_wait_read<0>();  // the staging stays until the TMA engine has read it
+  }
+  if (timed_out) atomicOr(&ea.ws.hdr->status, kFlagTimeout);
+  tc::fence_before_sync();
+  if constexpr (CG == 1) __syncthreads();
+  else cluster_sync();  // the pair's barriers and TMEM stay until both are done
+  tc::fence_after_sync();
+  if (warp == 1) {
+    if constexpr (CG == 1) tc::tmem_dealloc(tmem_base, 512);
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem_base) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ merge
+// 32 rows per CTA, the tiles of a row spread over 32 slices (one warp each, the rows its
+// lanes); the slices' pairs are combined in slice order.  Loss terms in FP64, summed per
+// CTA and by the last CTA in CTA order: a fixed order, so repeated calls agree bit by bit.
+constexpr int kSlices = 32;
+
+__global__ void __launch_bounds__(kSlices * 32) merge_kernel(const View ws, const Plan pl, const float z_alpha,
+                                                             const dspark_lce_out_t out) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float2 sp[kSlices][kMergeRows];
+  __shared__ double sd[32];
+  __shared__ int is_last;
+  const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
+  const int64_t r = int64_t(blockIdx.x) * kMergeRows + lane;
+  const int i = r < pl.R ? ws.index[r] : -1;
+  float m = -INFINITY, s = 0.f;
+  if (i >= 0) {
+#pragma unroll 4
+    for (int64_t t = sl; t < 2 * pl.fwd_tiles; t += kSlices) {
+      const float2 p = ws.part[size_t(t) * pl.Rp + i];
+      const float nm = fmaxf(m, p.x), ref = nm == -INFINITY ? 0.f : nm;
+      s = s * ex2(m - ref) + p.y * ex2(p.x - ref);
+      m = nm;
+    }
+  }
+  sp[sl][lane] = make_float2(m, s);
+  __syncthreads();
+  if (sl == 0) {
+    double term = 0.0;
+    float ce = 0.f, lse = 0.f;
+    if (i >= 0) {
+      for (int k = 1; k < kSlices; ++k) {
+        const float2 p = sp[k][lane];
+        const float nm = fmaxf(m, p.x), ref = nm == -INFINITY ? 0.f : nm;
+        s = s * ex2(m - ref) + p.y * ex2(p.x - ref);
+        m = nm;
+      }
+      const float lse2 = m + log2f(s);
+      ws.lse2[i] = lse2;
+      lse = lse2 * kLn2;
+      ce = fmaf(lse2, kLn2, -ws.zt[i]);
+      term = double(ws.w[i]) * (double(ce) + double(z_alpha) * double(lse) * double(lse));
+    }
+    if (r < pl.R) {
+      if (out.ce_rows) out.ce_rows[r] = ce;
+      if (out.lse_rows) out.lse_rows[r] = lse;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) term += __shfl_xor_sync(0xffffffffu, term, off);
+    if (lane == 0) {
+      ws.loss_part[blockIdx.x] = term;
+      __threadfence();
+      is_last = atomicAdd(&ws.hdr->done, 1u) == gridDim.x - 1;
+    }
+  }
+  __syncthreads();
+  if (!is_last || out.loss_num == nullptr) return;
+  __threadfence();
+  double acc = 0.0;
+  for (int64_t k = threadIdx.x; k < gridDim.x; k += blockDim.x) acc += __ldcg(ws.loss_part + k);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+  if (lane == 0) sd[sl] = acc;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double t = 0.0;
+    for (int k = 0; k < kSlices; ++k) t += sd[k];
+    *out.loss_num = float(t);
+  }
+}
+
+// ------------------------------------------------------------------ dhidden
+// The planes' sums in plane order, rounded once; rows without a label are zero.
+__global__ void __launch_bounds__(256) dhidden_kernel(const View ws, const Plan pl, uint16_t* dh, int64_t ld) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t h8 = pl.H / 8, n = pl.R * h8;
+  for (int64_t k = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; k < n; k += int64_t(gridDim.x) * blockDim.x) {
+    const int64_t r = k / h8, j = (k - r * h8) * 8;
+    const int i = ws.index[r];
+    uint4 o = make_uint4(0u, 0u, 0u, 0u);
+    if (i >= 0) {
+      float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      const float* src = ws.planes + size_t(i) * pl.H + j;
+#pragma unroll 2
+      for (int s = 0; s < pl.ksplit; ++s, src += size_t(pl.R) * pl.H) {
+        const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 4);
+        a[0] += x.x, a[1] += x.y, a[2] += x.z, a[3] += x.w;
+        a[4] += y.x, a[5] += y.y, a[6] += y.z, a[7] += y.w;
+      }
+      o = make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
+    }
+    *reinterpret_cast<uint4*>(dh + size_t(r) * ld + j) = o;
+  }
+}
+
+// ------------------------------------------------------------------ host side
+struct PdlLaunch {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[2];
+  PdlLaunch(int64_t grid, int threads, size_t smem, cudaStream_t s, int cluster = 1) {
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cluster > 1) {
+      at[1].id = cudaLaunchAttributeClusterDimension;
+      at[1].val.clusterDim.x = unsigned(cluster);
+      at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+      cfg.numAttrs = 2;
+    }
+  }
+};
+
+// A bf16 output written by tensor stores of 32-row, 64-column boxes (128-byte swizzle).
+bool make_out16_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld) {
+  return tc::make_map(m, base, rows, cols, ld, 64, 32);
+}
+
+template <int CG, int EPI>
+cudaError_t product_cg(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const Work& wk,
+                       const EpiArgs& ea, int bn, cudaStream_t s) {
+  auto kern = product_kernel<CG, EPI>;
+  constexpr size_t smem = smem_bytes<CG>();
+  // per device, so set on every call (it is a host-side table entry)
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  const int64_t W = int64_t(wk.m_tiles) * wk.n_tiles * wk.ksplit;
+  const int64_t grid = std::min<int64_t>(W, std::max(1, tc::sm_count() / CG)) * CG;
+  PdlLaunch l(grid, kThreads, smem, s, CG);
+  return cudaLaunchKernelEx(&l.cfg, kern, a, b, o, wk, ea, bn);
+}
+
+template <int EPI>
+cudaError_t product(const Plan& pl, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const Work& wk,
+                    const EpiArgs& ea, int bn, cudaStream_t s) {
+  return pl.cg == 2 ? product_cg<2, EPI>(a, b, o, wk, ea, bn, s) : product_cg<1, EPI>(a, b, o, wk, ea, bn, s);
+}
+
+int tiles(int64_t n, int64_t t) { return int(ceil_div(n, t)); }
+
+}  // namespace
+
+cudaError_t launch_fwd(const dspark_lce_problem_t& p, const dspark_lce_out_t& out, const Plan& pl, const View& ws,
+                       cudaStream_t s) {
+  const int64_t ctas = std::min<int64_t>(ceil_div(p.R, 8), 4 * kSlots);
+  const int64_t rows_per_cta = ceil_div(p.R, ctas);
+  prep_kernel<<<unsigned(ceil_div(p.R, rows_per_cta)), kPrepThreads, 0, s>>>(p, ws, out.num_tokens, rows_per_cta);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  CUtensorMap ma, mb;
+  if (!tc::make_map(&ma, ws.hsup, pl.Rp, p.H, p.H, 64, kBM) ||
+      !tc::make_map(&mb, p.weight, p.V, p.H, p.weight_ld, 64, pl.bn_fwd / pl.cg))
+    return cudaErrorInvalidValue;
+  Work wk{tiles(p.R, kBM * pl.cg), tiles(p.V, pl.bn_fwd), 1, tiles(p.H, BK), 16, 1, 0, &ws.hdr->n_valid};
+  EpiArgs ea{};
+  ea.ws = ws;
+  ea.Rp = pl.Rp;
+  ea.rows = int32_t(pl.Rp);
+  ea.n_cols = int32_t(p.V);
+  if ((e = product<kFwd>(pl, ma, mb, ma, wk, ea, pl.bn_fwd, s)) != cudaSuccess) return e;
+  PdlLaunch l(pl.merge_blocks, kSlices * 32, 0, s);
+  return cudaLaunchKernelEx(&l.cfg, merge_kernel, ws, pl, p.z_alpha, out);
+}
+
+cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& g, const Plan& pl, const View& ws,
+                       cudaStream_t s) {
+  const bool f32 = g.dweight_dtype == DSPARK_F32;
+  cudaError_t e;
+  CUtensorMap h_k, h_mn;
+  if (!tc::make_map(&h_k, ws.hsup, pl.Rp, p.H, p.H, 64, kBM) || !tc::make_map(&h_mn, ws.hsup, pl.Rp, p.H, p.H, 64, 64))
+    return cudaErrorInvalidValue;
+  for (int i = 0; i < pl.pieces; ++i) {
+    const int64_t v0 = int64_t(i) * pl.piece, n = std::min<int64_t>(pl.piece, p.V - v0);
+    const int64_t ldz = pl.piece;
+    const uint16_t* w0 = static_cast<const uint16_t*>(p.weight) + size_t(v0) * p.weight_ld;
+    CUtensorMap w_k, w_mn, z_out, z_k, z_mn, o;
+    if (!tc::make_map(&w_k, w0, n, p.H, p.weight_ld, 64, pl.bn_dz / pl.cg) ||
+        !make_out16_map(&z_out, ws.dz, pl.Rp, ldz, ldz))
+      return cudaErrorInvalidValue;
+    EpiArgs ea{};
+    ea.ws = ws;
+    ea.Rp = pl.Rp;
+    ea.rows = int32_t(pl.Rp);
+    ea.n_cols = int32_t(n);
+    ea.col0 = int32_t(v0);
+    ea.z_alpha = p.z_alpha;
+    ea.grad_scale = g.grad_scale;
+    const Work wz{tiles(p.R, kBM * pl.cg), tiles(n, pl.bn_dz), 1, tiles(p.H, BK), 16, 1, 0, &ws.hdr->n_valid};
+    if ((e = product<kDz>(pl, h_k, w_k, z_out, wz, ea, pl.bn_dz, s)) != cudaSuccess) return e;
+    if (g.dhidden) {
+      if (!tc::make_map(&w_mn, w0, n, p.H, p.weight_ld, 64, 64) || !tc::make_map(&z_k, ws.dz, pl.Rp, ldz, ldz, 64, kBM) ||
+          !tc::make_out_map(&o, ws.planes, pl.R, p.H, p.H, pl.ksplit, size_t(pl.R) * p.H))
+        return cudaErrorInvalidValue;
+      ea.n_cols = int32_t(p.H);
+      ea.add = i > 0;
+      const Work wh{tiles(p.R, kBM * pl.cg), tiles(p.H, pl.bn_h), pl.ksplit, tiles(n, BK), 8, 1, 0, &ws.hdr->n_valid};
+      if ((e = product<kDh>(pl, z_k, w_mn, o, wh, ea, pl.bn_h, s)) != cudaSuccess) return e;
+    }
+    if (g.dweight) {
+      void* d0 = static_cast<uint8_t*>(g.dweight) + size_t(v0) * g.dweight_ld * (f32 ? 4 : 2);
+      if (!tc::make_map(&z_mn, ws.dz, pl.Rp, ldz, ldz, 64, 64) ||
+          !(f32 ? tc::make_out_map(&o, d0, n, p.H, g.dweight_ld) : make_out16_map(&o, d0, n, p.H, g.dweight_ld)))
+        return cudaErrorInvalidValue;
+      ea.rows = int32_t(n);
+      ea.n_cols = int32_t(p.H);
+      ea.add = g.accumulate ? 1 : 0;
+      const Work ww{tiles(n, kBM * pl.cg), tiles(p.H, pl.bn_h), 1, tiles(p.R, BK), 8, 0, 1, &ws.hdr->n_valid};
+      e = f32 ? product<kDwF32>(pl, z_mn, h_mn, o, ww, ea, pl.bn_h, s)
+              : product<kDwBf16>(pl, z_mn, h_mn, o, ww, ea, pl.bn_h, s);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  if (g.dhidden) {
+    const int64_t blocks = std::min<int64_t>(ceil_div(p.R * (p.H / 8), 256), 8 * kSlots);
+    PdlLaunch l(blocks, 256, 0, s);
+    return cudaLaunchKernelEx(&l.cfg, dhidden_kernel, ws, pl, static_cast<uint16_t*>(g.dhidden), g.dhidden_ld);
+  }
+  return cudaSuccess;
+}
+
+}  // namespace lce
+}  // namespace dspark

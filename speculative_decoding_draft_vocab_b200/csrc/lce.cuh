@@ -1,0 +1,125 @@
+// Linear cross entropy (softmax cross entropy of hidden . weight^T, logits never kept):
+// the plan a shape gets, its workspace map and the launchers.
+#pragma once
+#include "internal.cuh"
+
+namespace dspark {
+namespace lce {
+
+constexpr int kBM = 128;                             // tile rows per CTA (TMEM lanes)
+constexpr int kSlots = 148;                          // SMs the plan assumes
+constexpr size_t kPieceBytes = size_t(256) << 20;    // bound on the kept piece of dz
+constexpr int kMergeRows = 32;                       // rows per CTA of the merge kernel
+
+struct WsLceHeader {
+  uint32_t status;     // device error bits
+  int32_t n_valid;     // labelled rows
+  uint32_t done;       // merge CTAs finished
+  uint32_t pad[61];
+};
+static_assert(sizeof(WsLceHeader) == 256, "header is one 256-byte line");
+
+// Everything about a call that follows from its sizes alone.
+struct Plan {
+  int64_t R, V, H;
+  int64_t Rp;          // R rounded up to a whole 64-row K chunk
+  int cg;              // CTAs per tile: 1, or a pair sharing one 256-row tile
+  int bn_fwd;          // vocabulary columns per tile of the forward product
+  int bn_dz;           // the same where dz is stored (whole 64-column boxes)
+  int bn_h;            // hidden columns per tile of the gradient products
+  int64_t fwd_tiles;   // vocabulary tiles of the forward product
+  int64_t piece;       // vocabulary columns per piece of the backward
+  int pieces;
+  int ksplit;          // K splits of the hidden gradient (planes of partial sums)
+  int64_t merge_blocks;
+};
+
+struct View {
+  WsLceHeader* hdr;
+  double* loss_part;   // [merge_blocks]
+  int32_t* list;       // [R] labelled rows in row order
+  int32_t* index;      // [R] position of a row in `list`, -1 without a label
+  int32_t* tok;        // [R] label of the i-th labelled row
+  float* w;            // [R] weight of the i-th labelled row
+  float* lse2;         // [R] base-2 logsumexp of the i-th labelled row
+  float* zt;           // [R] logit at the label
+  uint16_t* hsup;      // [Rp][H] bf16 labelled hidden rows, compact, zeros up to a whole chunk
+  float2* part;        // [2 fwd_tiles][Rp] (base-2 maximum, sum) of a row's columns in half a tile
+  uint16_t* dz;        // [Rp][piece] bf16 piece of dL/dlogits
+  float* planes;       // [ksplit][R][H] partial sums of the hidden gradient
+};
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+inline Plan make_plan(int64_t R, int64_t V, int64_t H) {
+  Plan p{};
+  p.R = R, p.V = V, p.H = H;
+  p.Rp = ceil_div(R, 64) * 64;
+  p.cg = R > kBM ? 2 : 1;
+  p.bn_fwd = p.bn_dz = 256;
+  p.bn_h = H > 128 ? 256 : 128;
+  p.fwd_tiles = ceil_div(V, p.bn_fwd);
+  const int64_t most = std::max<int64_t>(256, int64_t(kPieceBytes / (2 * size_t(p.Rp))) / 256 * 256);
+  p.pieces = int(ceil_div(V, most));
+  p.piece = ceil_div(ceil_div(V, p.pieces), 256) * 256;
+  p.pieces = int(ceil_div(V, p.piece));
+  // few row and hidden tiles: the K range (the piece's vocabulary) is split so that every
+  // SM has work, each split at least eight 64-wide chunks long
+  const int64_t tiles = ceil_div(R, kBM * p.cg) * ceil_div(H, p.bn_h);
+  p.ksplit = int(std::max<int64_t>(1, std::min<int64_t>(kSlots / p.cg / tiles, p.piece / 512)));
+  p.merge_blocks = ceil_div(R, kMergeRows);
+  return p;
+}
+
+struct Offsets {
+  size_t hdr, loss_part, list, index, tok, w, lse2, zt, hsup, part, fwd_bytes, dz, planes, bytes;
+};
+
+inline Offsets offsets(const Plan& p, bool bwd, bool dhidden) {
+  Offsets o{};
+  size_t off = 0;
+  const size_t R = size_t(p.R), Rp = size_t(p.Rp);
+  auto take = [&](size_t& at, size_t n) { at = off; off = align256(off + n); };
+  take(o.hdr, sizeof(WsLceHeader));
+  take(o.loss_part, sizeof(double) * size_t(p.merge_blocks));
+  take(o.list, 4 * R);
+  take(o.index, 4 * R);
+  take(o.tok, 4 * R);
+  take(o.w, 4 * R);
+  take(o.lse2, 4 * R);
+  take(o.zt, 4 * R);
+  take(o.hsup, 2 * Rp * size_t(p.H));
+  take(o.part, sizeof(float2) * 2 * size_t(p.fwd_tiles) * Rp);
+  o.fwd_bytes = off;
+  take(o.dz, bwd ? 2 * Rp * size_t(p.piece) : 0);
+  take(o.planes, bwd && dhidden ? sizeof(float) * size_t(p.ksplit) * R * size_t(p.H) : 0);
+  o.bytes = off;
+  return o;
+}
+
+inline View view(void* base, const Plan& p) {
+  const Offsets o = offsets(p, true, true);
+  uint8_t* b = static_cast<uint8_t*>(base);
+  View v{};
+  v.hdr = reinterpret_cast<WsLceHeader*>(b + o.hdr);
+  v.loss_part = reinterpret_cast<double*>(b + o.loss_part);
+  v.list = reinterpret_cast<int32_t*>(b + o.list);
+  v.index = reinterpret_cast<int32_t*>(b + o.index);
+  v.tok = reinterpret_cast<int32_t*>(b + o.tok);
+  v.w = reinterpret_cast<float*>(b + o.w);
+  v.lse2 = reinterpret_cast<float*>(b + o.lse2);
+  v.zt = reinterpret_cast<float*>(b + o.zt);
+  v.hsup = reinterpret_cast<uint16_t*>(b + o.hsup);
+  v.part = reinterpret_cast<float2*>(b + o.part);
+  v.dz = reinterpret_cast<uint16_t*>(b + o.dz);
+  v.planes = reinterpret_cast<float*>(b + o.planes);
+  return v;
+}
+
+cudaError_t launch_fwd(const dspark_lce_problem_t& p, const dspark_lce_out_t& out, const Plan& plan, const View& ws,
+                       cudaStream_t s);
+cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& g, const Plan& plan, const View& ws,
+                       cudaStream_t s);
+
+}  // namespace lce
+}  // namespace dspark

@@ -395,3 +395,130 @@ def tp_group_emulated(inp: DSparkInputs, tp_size: int, grads: bool = True, rows:
         for r in ranks:
             r.heads_bwd(de_all)
     return ranks
+
+
+# ------------------------------------------------- training-step operators beside the loss
+def _matrix(t: Optional[torch.Tensor], dtypes, name):
+    """A CUDA matrix whose rows are contiguous (any row stride); returns its row stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] < 1 or t.shape[1] < 1:
+        raise ValueError(f"{name} must be a matrix with at least one row and one column")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.shape[1] if t.shape[0] == 1 else t.stride(0)
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the call's tensors on {dev}")
+
+
+_ABI_DTYPE = {torch.float32: abi.DSPARK_F32, torch.bfloat16: abi.DSPARK_BF16}
+
+
+class _DeviceCall:
+    """What the prepared calls below share: a workspace, and launches on the current stream
+    of the device that holds the tensors, whichever device is current."""
+
+    def _workspace(self, nbytes: int) -> None:
+        if nbytes == 0:
+            raise abi.DSparkError(abi.DSPARK_ERR_UNSUPPORTED, type(self).__name__)
+        self.ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=self.device)
+        self.ws_ptr, self.ws_len = _aligned_ws(self.ws)
+
+    def _run(self, fn, where, stream, *args) -> None:
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return self._run(fn, where, stream, *args)
+        s = torch.cuda.current_stream().cuda_stream if stream is None else stream
+        abi.check(fn(*args, ctypes.c_void_p(s)), where)
+
+    def check_status(self, stream=None) -> int:
+        with torch.cuda.device(self.device):
+            s = torch.cuda.current_stream().cuda_stream if stream is None else stream
+            return int(abi.dspark_check_status(self.ws_ptr, ctypes.c_void_p(s)))
+
+
+class LinearCE(_DeviceCall):
+    """A prepared linear cross entropy: the loss of ``hidden @ weight.T`` against
+    ``targets`` over the whole vocabulary and its gradients, the logits never kept
+    (dspark_lce_fwd, dspark_lce_bwd).
+
+    ``hidden`` [R, H] and ``weight`` [V, H] are bf16 with contiguous rows, ``targets`` [R]
+    int64, ``row_weight`` [R] fp32.  forward() writes ``loss_num``, ``num_tokens``,
+    ``ce_rows``, ``lse_rows``; backward() writes ``dhidden`` (bf16) and ``dweight``
+    (``dweight_dtype``; with ``accumulate`` added to, fp32 only).  Pass tensors for
+    ``dhidden`` / ``dweight`` to have them written there, False to leave them out.
+    ``grad_scale`` [1] fp32 may be filled before backward().
+    """
+
+    def __init__(self, hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                 row_weight: Optional[torch.Tensor] = None, ignore_index: int = -100, z_alpha: float = 0.0,
+                 dhidden=True, dweight=True, dweight_dtype: torch.dtype = torch.bfloat16,
+                 accumulate: bool = False):
+        bf = (torch.bfloat16,)
+        p = abi.dspark_lce_problem_t()
+        p.hidden_ld, p.weight_ld = _matrix(hidden, bf, "hidden"), _matrix(weight, bf, "weight")
+        (R, H), V = hidden.shape, weight.shape[0]
+        if weight.shape[1] != H:
+            raise ValueError(f"weight has {weight.shape[1]} columns, hidden {H}")
+        _need(targets, torch.int64, "targets")
+        _need(row_weight, torch.float32, "row_weight")
+        if targets.numel() != R or (row_weight is not None and row_weight.numel() != R):
+            raise ValueError(f"targets and row_weight must hold {R} values")
+        self.device = dev = hidden.device
+        _same_device(dev, weight=weight, targets=targets, row_weight=row_weight)
+        p.R, p.V, p.H = R, V, H
+        p.hidden, p.weight, p.targets = _ptr(hidden), _ptr(weight), _ptr(targets)
+        p.ignore_index, p.row_weight, p.z_alpha = ignore_index, _ptr(row_weight), z_alpha
+        self.prob = p
+        self._keep = (hidden, weight, targets, row_weight)
+        f32 = dict(dtype=torch.float32, device=dev)
+        self.loss_num = torch.zeros(1, **f32)
+        self.num_tokens = torch.zeros(1, dtype=torch.int64, device=dev)
+        self.ce_rows, self.lse_rows = torch.zeros(R, **f32), torch.zeros(R, **f32)
+        self.grad_scale = torch.ones(1, **f32)
+        self.dhidden = self.dweight = self.grads = None
+        if dhidden is not False and dhidden is not None:
+            self.dhidden = torch.empty(R, H, dtype=torch.bfloat16, device=dev) if dhidden is True else dhidden
+        if dweight is not False and dweight is not None:
+            if dweight is True:
+                dweight = (torch.zeros if accumulate else torch.empty)(V, H, dtype=dweight_dtype, device=dev)
+            self.dweight = dweight
+        if self.dhidden is not None or self.dweight is not None:
+            g = abi.dspark_lce_grads_t()
+            g.grad_scale = _ptr(self.grad_scale)
+            if self.dhidden is not None:
+                g.dhidden_ld = _matrix(self.dhidden, bf, "dhidden")
+                if self.dhidden.shape != hidden.shape:
+                    raise ValueError("dhidden must have the shape of hidden")
+                g.dhidden = _ptr(self.dhidden)
+            if self.dweight is not None:
+                g.dweight_ld = _matrix(self.dweight, tuple(_ABI_DTYPE), "dweight")
+                if self.dweight.shape != weight.shape:
+                    raise ValueError("dweight must have the shape of weight")
+                g.dweight, g.dweight_dtype = _ptr(self.dweight), _ABI_DTYPE[self.dweight.dtype]
+                g.accumulate = 1 if accumulate else 0
+            _same_device(dev, dhidden=self.dhidden, dweight=self.dweight)
+            self.grads = g
+        o = abi.dspark_lce_out_t()
+        o.loss_num, o.num_tokens = _ptr(self.loss_num), _ptr(self.num_tokens)
+        o.ce_rows, o.lse_rows = _ptr(self.ce_rows), _ptr(self.lse_rows)
+        self.out = o
+        self._workspace(int(abi.dspark_lce_workspace_size(
+            ctypes.byref(p), ctypes.byref(self.grads) if self.grads is not None else None)))
+
+    def forward(self, stream=None) -> None:
+        self._run(abi.dspark_lce_fwd, "dspark_lce_fwd", stream, ctypes.byref(self.prob), ctypes.byref(self.out),
+                  self.ws_ptr, self.ws_len)
+
+    def backward(self, stream=None) -> None:
+        """The gradients of the last forward(), times ``grad_scale``."""
+        if self.grads is None:
+            raise ValueError("this call was built without gradients")
+        self._run(abi.dspark_lce_bwd, "dspark_lce_bwd", stream, ctypes.byref(self.prob), ctypes.byref(self.grads),
+                  self.ws_ptr, self.ws_len)
