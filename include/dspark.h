@@ -404,6 +404,89 @@ DSPARK_API dspark_status_t dspark_lce_fwd(const dspark_lce_problem_t* prob, cons
 DSPARK_API dspark_status_t dspark_lce_bwd(const dspark_lce_problem_t* prob, const dspark_lce_grads_t* grads, void* ws,
                                           size_t ws_bytes, dspark_stream_t stream);
 
+/*
+ * Scaled embedding lookup and its gradient (the gather that feeds a drafter, and the table
+ * gradient dW1 of dspark_grads_t in a form whose sums have a fixed order).
+ *   out_r    = scale * table[id_r]                       (rounded once to the table's type)
+ *   dtable_i = scale * sum over rows r with id_r = i of dout_r, added in row order in FP32
+ * A row whose `valid` is 0 gives a zero output row and no gradient; its id is not looked at.
+ * An id outside [0, Vt) raises DSPARK_ERR_ID_OUT_OF_RANGE and counts as not valid.
+ *
+ * dspark_embed_bwd sorts the rows by id (a stable radix sort on the device), sums each id's
+ * rows and writes each touched table row once.  Without `accumulate` every other row is
+ * zeroed; with it the sums are added and other rows are neither read nor written.  Two runs
+ * give the same bits.
+ *
+ * `dtype` is the type of table and out, or of dout.  D, the leading dimensions and the
+ * matrix pointers obey the 16-byte rule above; Vt and R are free.  More than 2^24 rows,
+ * 2^30 table rows or 2^20 columns are DSPARK_ERR_UNSUPPORTED.
+ */
+typedef struct {
+  int64_t R, Vt, D;            /* rows, table rows, table columns                       */
+  int64_t dtype;               /* dspark_dtype_t                                        */
+  const int64_t* ids;          /* [R]                                                   */
+  const uint8_t* valid;        /* [R] nonzero = looked up, or NULL = all                */
+  float scale;
+} dspark_embed_problem_t;
+
+/* Bytes of device workspace: for the lookup (grads 0) or the gradient (grads nonzero).
+ * 0 on an invalid problem. */
+DSPARK_API size_t dspark_embed_workspace_size(const dspark_embed_problem_t* prob, int64_t grads);
+
+/* out [R, D] (row stride out_ld) from table [Vt, D] (row stride table_ld).  out must not
+ * overlap table. */
+DSPARK_API dspark_status_t dspark_embed_fwd(const dspark_embed_problem_t* prob, const void* table, int64_t table_ld,
+                                            void* out, int64_t out_ld, void* ws, size_t ws_bytes,
+                                            dspark_stream_t stream);
+
+/* dtable [Vt, D] (row stride dtable_ld, type dtable_dtype: DSPARK_F32 or DSPARK_BF16) from
+ * dout [R, D] (row stride dout_ld).  accumulate needs an FP32 table (a bf16 sum over calls
+ * would lose its small terms): DSPARK_ERR_UNSUPPORTED otherwise. */
+DSPARK_API dspark_status_t dspark_embed_bwd(const dspark_embed_problem_t* prob, const void* dout, int64_t dout_ld,
+                                            void* dtable, int64_t dtable_ld, int64_t dtable_dtype,
+                                            int64_t accumulate, void* ws, size_t ws_bytes, dspark_stream_t stream);
+
+/*
+ * Global gradient norm and clipping over many tensors (the gradients above, say).
+ *   sumsq = sum over all tensors of x^2,  norm = sqrt(sumsq)
+ *   coef  = min(1, max_norm / (norm + 1e-6)), or 1 where the norm is not finite
+ *   dst_t = coef * src_t, rounded once to the tensor's type
+ * A norm that is not finite leaves the values as they are (the caller sees the norm and
+ * skips its step).  Sums are FP64 in a fixed order: two runs give the same bits.
+ *
+ * `tensors` is a HOST array of `count` descriptors, read during the call.  src and dst are
+ * device pointers of n contiguous elements, aligned to their element; n may be 0; dst may
+ * equal src (in place; nothing is written then if coef is 1), or be a separate buffer that
+ * overlaps no src.  The same tensor must not be listed twice.
+ *
+ * dspark_grad_clip does both steps on one device.  Where the gradients are spread over
+ * ranks (a vocabulary-parallel dW2), dspark_grad_sumsq writes this rank's FP64 sum, the
+ * caller all-reduces it, and dspark_grad_scale clips by the reduced sum.
+ */
+typedef struct {
+  const void* src;
+  void* dst;                   /* not looked at by dspark_grad_sumsq                    */
+  int64_t n;
+  int64_t dtype;               /* dspark_dtype_t                                        */
+} dspark_tensor_t;
+
+/* Bytes of device workspace for `count` tensors (0 on a count below 1 or above 2^20). */
+DSPARK_API size_t dspark_grad_workspace_size(int64_t count);
+
+/* sumsq [1] (device, FP64). */
+DSPARK_API dspark_status_t dspark_grad_sumsq(const dspark_tensor_t* tensors, int64_t count, double* sumsq, void* ws,
+                                             size_t ws_bytes, dspark_stream_t stream);
+
+/* Clips by sumsq [1] (device, FP64); writes norm [1] and coef [1] (device, FP32) if
+ * non-NULL.  max_norm > 0. */
+DSPARK_API dspark_status_t dspark_grad_scale(const dspark_tensor_t* tensors, int64_t count, const double* sumsq,
+                                             float max_norm, float* norm, float* coef, void* ws, size_t ws_bytes,
+                                             dspark_stream_t stream);
+
+/* Both steps. */
+DSPARK_API dspark_status_t dspark_grad_clip(const dspark_tensor_t* tensors, int64_t count, float max_norm, float* norm,
+                                            float* coef, void* ws, size_t ws_bytes, dspark_stream_t stream);
+
 /* Synchronises `stream` and returns the first device-side error recorded in `ws`
  * by the last call that used it (DSPARK_OK if none). */
 DSPARK_API dspark_status_t dspark_check_status(const void* ws, dspark_stream_t stream);

@@ -112,6 +112,17 @@ class dspark_lce_grads_t(ctypes.Structure):
     ]
 
 
+class dspark_embed_problem_t(ctypes.Structure):
+    _fields_ = [
+        ("R", c_i64), ("Vt", c_i64), ("D", c_i64), ("dtype", c_i64),
+        ("ids", c_vp), ("valid", c_vp), ("scale", ctypes.c_float),
+    ]
+
+
+class dspark_tensor_t(ctypes.Structure):
+    _fields_ = [("src", c_vp), ("dst", c_vp), ("n", c_i64), ("dtype", c_i64)]
+
+
 # floats per row of the two exchange records of the vocabulary-parallel path
 DSPARK_TP_REC1_FLOATS = 8
 DSPARK_TP_REC2_FLOATS = 4
@@ -148,6 +159,22 @@ lib.dspark_lce_fwd.argtypes = [P(dspark_lce_problem_t), P(dspark_lce_out_t), c_v
 lib.dspark_lce_fwd.restype = ctypes.c_int
 lib.dspark_lce_bwd.argtypes = [P(dspark_lce_problem_t), P(dspark_lce_grads_t), c_vp, ctypes.c_size_t, c_vp]
 lib.dspark_lce_bwd.restype = ctypes.c_int
+lib.dspark_embed_workspace_size.argtypes = [P(dspark_embed_problem_t), c_i64]
+lib.dspark_embed_workspace_size.restype = ctypes.c_size_t
+lib.dspark_embed_fwd.argtypes = [P(dspark_embed_problem_t), c_vp, c_i64, c_vp, c_i64, c_vp, ctypes.c_size_t, c_vp]
+lib.dspark_embed_fwd.restype = ctypes.c_int
+lib.dspark_embed_bwd.argtypes = [P(dspark_embed_problem_t), c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp,
+                                 ctypes.c_size_t, c_vp]
+lib.dspark_embed_bwd.restype = ctypes.c_int
+lib.dspark_grad_workspace_size.argtypes = [c_i64]
+lib.dspark_grad_workspace_size.restype = ctypes.c_size_t
+lib.dspark_grad_sumsq.argtypes = [P(dspark_tensor_t), c_i64, c_vp, c_vp, ctypes.c_size_t, c_vp]
+lib.dspark_grad_sumsq.restype = ctypes.c_int
+lib.dspark_grad_scale.argtypes = [P(dspark_tensor_t), c_i64, c_vp, ctypes.c_float, c_vp, c_vp, c_vp,
+                                  ctypes.c_size_t, c_vp]
+lib.dspark_grad_scale.restype = ctypes.c_int
+lib.dspark_grad_clip.argtypes = [P(dspark_tensor_t), c_i64, ctypes.c_float, c_vp, c_vp, c_vp, ctypes.c_size_t, c_vp]
+lib.dspark_grad_clip.restype = ctypes.c_int
 lib.dspark_check_status.argtypes = [c_vp, c_vp]
 lib.dspark_check_status.restype = ctypes.c_int
 lib.dspark_status_string.argtypes = [ctypes.c_int]
@@ -172,6 +199,13 @@ dspark_tp_heads_bwd = lib.dspark_tp_heads_bwd
 dspark_lce_workspace_size = lib.dspark_lce_workspace_size
 dspark_lce_fwd = lib.dspark_lce_fwd
 dspark_lce_bwd = lib.dspark_lce_bwd
+dspark_embed_workspace_size = lib.dspark_embed_workspace_size
+dspark_embed_fwd = lib.dspark_embed_fwd
+dspark_embed_bwd = lib.dspark_embed_bwd
+dspark_grad_workspace_size = lib.dspark_grad_workspace_size
+dspark_grad_sumsq = lib.dspark_grad_sumsq
+dspark_grad_scale = lib.dspark_grad_scale
+dspark_grad_clip = lib.dspark_grad_clip
 dspark_check_status = lib.dspark_check_status
 dspark_status_string = lib.dspark_status_string
 dspark_last_cuda_error = lib.dspark_last_cuda_error

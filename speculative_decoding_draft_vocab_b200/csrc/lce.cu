@@ -24,6 +24,7 @@
 #include <algorithm>
 
 #include "lce.cuh"
+#include "pdl.cuh"
 #include "tc_host.cuh"
 
 namespace dspark {
@@ -33,9 +34,6 @@ namespace {
 using tc::BK;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;"); }
 
 // ------------------------------------------------------------------ prep
 // Each CTA takes a contiguous run of rows, counts the labelled rows before it (the labels
@@ -709,27 +707,6 @@ __global__ void __launch_bounds__(256) dhidden_kernel(const View ws, const Plan 
 }
 
 // ------------------------------------------------------------------ host side
-struct PdlLaunch {
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at[2];
-  PdlLaunch(int64_t grid, int threads, size_t smem, cudaStream_t s, int cluster = 1) {
-    cfg.gridDim = dim3(unsigned(grid));
-    cfg.blockDim = dim3(unsigned(threads));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cluster > 1) {
-      at[1].id = cudaLaunchAttributeClusterDimension;
-      at[1].val.clusterDim.x = unsigned(cluster);
-      at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-      cfg.numAttrs = 2;
-    }
-  }
-};
-
 // A bf16 output written by tensor stores of 32-row, 64-column boxes (128-byte swizzle).
 bool make_out16_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld) {
   return tc::make_map(m, base, rows, cols, ld, 64, 32);

@@ -1,0 +1,114 @@
+// The embedding and gradient-clipping operators: workspace maps and launchers.
+#pragma once
+#include "internal.cuh"
+
+namespace dspark {
+
+// ------------------------------------------------------------------ embedding
+namespace embed {
+
+constexpr int kSortThreads = 512;
+constexpr int kSortItems = 8;                          // per thread and chunk
+constexpr int kSortChunk = kSortThreads * kSortItems;  // rows ranked at a time
+constexpr int kSortCtas = 128;                         // at most: a CTA sorts a run of chunks
+constexpr int kDigitBits = 9;
+constexpr int kDigits = 1 << kDigitBits;
+
+struct WsEmbedHeader {
+  uint32_t status;  // device error bits
+  uint32_t pad[63];
+};
+static_assert(sizeof(WsEmbedHeader) == 256, "header is one 256-byte line");
+
+struct Plan {
+  int64_t R, Vt, D;
+  int bits, passes;    // key bits and radix passes
+  int64_t run;         // rows per sorting CTA (whole chunks)
+  int ctas;            // sorting CTAs
+  int window;          // sorted rows per partial sum
+  int64_t windows;
+};
+
+inline Plan make_plan(int64_t R, int64_t Vt, int64_t D, bool f32) {
+  Plan p{};
+  p.R = R, p.Vt = Vt, p.D = D;
+  p.bits = 1;
+  while ((int64_t(1) << p.bits) <= Vt) ++p.bits;  // keys 0 .. Vt (Vt: dropped rows)
+  p.passes = (p.bits + kDigitBits - 1) / kDigitBits;
+  const int64_t chunks = (R + kSortChunk - 1) / kSortChunk;
+  p.run = (chunks + kSortCtas - 1) / kSortCtas * kSortChunk;
+  p.ctas = int((R + p.run - 1) / p.run);
+  // windows of 8 to 512 sorted rows: as long as about 32 warps per SM still have one each
+  const int64_t cols = f32 ? 128 : 256, blocks = (D + cols - 1) / cols;
+  p.window = 8;
+  while (p.window < 512 && (R / (2 * p.window)) * blocks >= 148 * 32) p.window *= 2;
+  p.windows = (R + p.window - 1) / p.window;
+  return p;
+}
+
+struct View {
+  WsEmbedHeader* hdr;
+  uint32_t* counts;   // [ctas][kDigits] digit counts of the sorting CTAs' runs
+  uint32_t* key[2];   // [R] ids, sorted back and forth
+  uint32_t* row[2];   // [R] the rows they came with
+  float* part;        // [windows][2][D] sums of the segments that cross a window's ends
+  size_t bytes;
+};
+
+inline View view(void* base, const Plan& p) {
+  View v{};
+  size_t off = 0;
+  uint8_t* b = static_cast<uint8_t*>(base);
+  auto take = [&](size_t n) { uint8_t* at = b + off; off = align256(off + n); return at; };
+  v.hdr = reinterpret_cast<WsEmbedHeader*>(take(sizeof(WsEmbedHeader)));
+  v.counts = reinterpret_cast<uint32_t*>(take(4 * size_t(p.ctas) * kDigits));
+  for (int i = 0; i < 2; ++i) v.key[i] = reinterpret_cast<uint32_t*>(take(4 * size_t(p.R)));
+  for (int i = 0; i < 2; ++i) v.row[i] = reinterpret_cast<uint32_t*>(take(4 * size_t(p.R)));
+  v.part = reinterpret_cast<float*>(take(sizeof(float) * 2 * size_t(p.windows) * size_t(p.D)));
+  v.bytes = off;
+  return v;
+}
+
+struct FwdArgs {
+  dspark_embed_problem_t p;
+  const void* table;
+  int64_t table_ld;
+  void* out;
+  int64_t out_ld;
+  WsEmbedHeader* hdr;
+};
+struct BwdArgs {
+  dspark_embed_problem_t p;
+  const void* dout;
+  int64_t dout_ld;
+  void* dtable;
+  int64_t dtable_ld;
+  int32_t table_f32, accumulate;
+  Plan plan;
+  View ws;
+};
+cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t s);
+cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t s);
+
+}  // namespace embed
+
+// ------------------------------------------------------------------ gradient clipping
+namespace clip {
+
+constexpr int kMaxTensors = 500;   // descriptors per launch (kernel parameters)
+constexpr int kGrid = 148 * 8;     // CTAs of a launch, at most
+constexpr int kThreads = 256;
+constexpr int64_t kChunk = 8192;   // elements a CTA takes at a time
+
+inline int64_t launches(int64_t count) { return (count + kMaxTensors - 1) / kMaxTensors; }
+// workspace: 256-byte header, then one FP64 partial sum per CTA and launch
+inline size_t ws_bytes(int64_t count) { return align256(256 + sizeof(double) * size_t(launches(count)) * kGrid); }
+
+cudaError_t launch_sumsq(const dspark_tensor_t* t, int64_t count, void* ws, cudaStream_t s, int64_t* partials);
+cudaError_t launch_total(const void* ws, int64_t partials, double* sumsq, cudaStream_t s);
+// by sumsq, or (null) by the partial sums in ws
+cudaError_t launch_scale(const dspark_tensor_t* t, int64_t count, const double* sumsq, int64_t partials,
+                         float max_norm, float* norm, float* coef, void* ws, cudaStream_t s);
+
+}  // namespace clip
+}  // namespace dspark

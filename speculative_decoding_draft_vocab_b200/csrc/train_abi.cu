@@ -2,6 +2,7 @@
 // validation, workspace carving and the launches.  No allocation, no synchronisation.
 #include "internal.cuh"
 #include "lce.cuh"
+#include "train.cuh"
 
 using namespace dspark;
 
@@ -32,6 +33,46 @@ dspark_status_t check_ws(const void* ws, size_t have, size_t need) {
   if (ws == nullptr) return DSPARK_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return DSPARK_ERR_ALIGNMENT;
   return have < need ? DSPARK_ERR_WORKSPACE : DSPARK_OK;
+}
+
+inline bool is_dtype(int64_t d) { return d == DSPARK_F32 || d == DSPARK_BF16; }
+inline int64_t elem_size(int64_t d) { return d == DSPARK_BF16 ? 2 : 4; }
+
+dspark_status_t check_embed(const dspark_embed_problem_t* p) {
+  if (p == nullptr || p->R <= 0 || p->Vt <= 0 || p->D <= 0 || !is_dtype(p->dtype)) return DSPARK_ERR_INVALID_ARG;
+  if (p->R > (int64_t(1) << 24) || p->Vt > (int64_t(1) << 30) || p->D > (int64_t(1) << 20)) return DSPARK_ERR_UNSUPPORTED;
+  return DSPARK_OK;
+}
+
+dspark_status_t check_matrix(const void* m, int64_t ld, int64_t cols, int64_t dtype) {
+  if (m == nullptr || ld < cols) return DSPARK_ERR_INVALID_ARG;
+  const int64_t es = elem_size(dtype);
+  return !aligned16(m) || (ld * es) % 16 || (cols * es) % 16 ? DSPARK_ERR_ALIGNMENT : DSPARK_OK;
+}
+
+embed::Plan embed_plan(const dspark_embed_problem_t* p) {
+  return embed::make_plan(p->R, p->Vt, p->D, p->dtype == DSPARK_F32);
+}
+
+dspark_status_t check_tensors(const dspark_tensor_t* t, int64_t count, bool dst) {
+  if (t == nullptr || count < 1) return DSPARK_ERR_INVALID_ARG;
+  if (count > (int64_t(1) << 20)) return DSPARK_ERR_UNSUPPORTED;
+  for (int64_t i = 0; i < count; ++i) {
+    if (t[i].n < 0 || !is_dtype(t[i].dtype)) return DSPARK_ERR_INVALID_ARG;
+    if (t[i].n > (int64_t(1) << 40)) return DSPARK_ERR_UNSUPPORTED;
+    if (t[i].n == 0) continue;
+    if (t[i].src == nullptr || (dst && t[i].dst == nullptr)) return DSPARK_ERR_INVALID_ARG;
+    const uintptr_t m = uintptr_t(elem_size(t[i].dtype) - 1);
+    if ((reinterpret_cast<uintptr_t>(t[i].src) & m) || (dst && (reinterpret_cast<uintptr_t>(t[i].dst) & m)))
+      return DSPARK_ERR_ALIGNMENT;
+  }
+  // a launch numbers the chunks of its tensors in 32 bits
+  for (int64_t i = 0; i < count; i += clip::kMaxTensors) {
+    int64_t chunks = 0;
+    for (int64_t k = i; k < count && k < i + clip::kMaxTensors; ++k) chunks += (t[k].n + clip::kChunk - 1) / clip::kChunk;
+    if (chunks > (int64_t(1) << 30)) return DSPARK_ERR_UNSUPPORTED;
+  }
+  return DSPARK_OK;
 }
 
 }  // namespace
@@ -73,6 +114,83 @@ dspark_status_t dspark_lce_bwd(const dspark_lce_problem_t* prob, const dspark_lc
   if ((st = check_ws(ws, ws_bytes, dspark_lce_workspace_size(prob, grads))) != DSPARK_OK) return st;
   const lce::Plan plan = lce::make_plan(prob->R, prob->V, prob->H);
   return cuda_status(lce::launch_bwd(*prob, *grads, plan, lce::view(ws, plan), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t dspark_embed_workspace_size(const dspark_embed_problem_t* prob, int64_t grads) {
+  if (check_embed(prob) != DSPARK_OK) return 0;
+  return grads ? embed::view(nullptr, embed_plan(prob)).bytes : sizeof(embed::WsEmbedHeader);
+}
+
+dspark_status_t dspark_embed_fwd(const dspark_embed_problem_t* prob, const void* table, int64_t table_ld, void* out,
+                                 int64_t out_ld, void* ws, size_t ws_bytes, dspark_stream_t stream) {
+  dspark_status_t st = check_embed(prob);
+  if (st != DSPARK_OK) return st;
+  if (prob->ids == nullptr) return DSPARK_ERR_INVALID_ARG;
+  if ((st = check_matrix(table, table_ld, prob->D, prob->dtype)) != DSPARK_OK) return st;
+  if ((st = check_matrix(out, out_ld, prob->D, prob->dtype)) != DSPARK_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, dspark_embed_workspace_size(prob, 0))) != DSPARK_OK) return st;
+  const embed::FwdArgs a{*prob, table, table_ld, out, out_ld, static_cast<embed::WsEmbedHeader*>(ws)};
+  return cuda_status(embed::launch_fwd(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dspark_status_t dspark_embed_bwd(const dspark_embed_problem_t* prob, const void* dout, int64_t dout_ld, void* dtable,
+                                 int64_t dtable_ld, int64_t dtable_dtype, int64_t accumulate, void* ws,
+                                 size_t ws_bytes, dspark_stream_t stream) {
+  dspark_status_t st = check_embed(prob);
+  if (st != DSPARK_OK) return st;
+  if (prob->ids == nullptr || !is_dtype(dtable_dtype)) return DSPARK_ERR_INVALID_ARG;
+  if (accumulate && dtable_dtype != DSPARK_F32) return DSPARK_ERR_UNSUPPORTED;
+  if ((st = check_matrix(dout, dout_ld, prob->D, prob->dtype)) != DSPARK_OK) return st;
+  if ((st = check_matrix(dtable, dtable_ld, prob->D, dtable_dtype)) != DSPARK_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, dspark_embed_workspace_size(prob, 1))) != DSPARK_OK) return st;
+  embed::BwdArgs a{};
+  a.p = *prob;
+  a.dout = dout, a.dout_ld = dout_ld;
+  a.dtable = dtable, a.dtable_ld = dtable_ld;
+  a.table_f32 = dtable_dtype == DSPARK_F32;
+  a.accumulate = accumulate ? 1 : 0;
+  a.plan = embed_plan(prob);
+  a.ws = embed::view(ws, a.plan);
+  return cuda_status(embed::launch_bwd(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t dspark_grad_workspace_size(int64_t count) {
+  return count < 1 || count > (int64_t(1) << 20) ? 0 : clip::ws_bytes(count);
+}
+
+dspark_status_t dspark_grad_sumsq(const dspark_tensor_t* tensors, int64_t count, double* sumsq, void* ws,
+                                  size_t ws_bytes, dspark_stream_t stream) {
+  dspark_status_t st = check_tensors(tensors, count, false);
+  if (st != DSPARK_OK) return st;
+  if (sumsq == nullptr) return DSPARK_ERR_INVALID_ARG;
+  if ((st = check_ws(ws, ws_bytes, clip::ws_bytes(count))) != DSPARK_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int64_t n = 0;
+  const cudaError_t e = clip::launch_sumsq(tensors, count, ws, s, &n);
+  return cuda_status(e != cudaSuccess ? e : clip::launch_total(ws, n, sumsq, s));
+}
+
+dspark_status_t dspark_grad_scale(const dspark_tensor_t* tensors, int64_t count, const double* sumsq, float max_norm,
+                                  float* norm, float* coef, void* ws, size_t ws_bytes, dspark_stream_t stream) {
+  dspark_status_t st = check_tensors(tensors, count, true);
+  if (st != DSPARK_OK) return st;
+  if (sumsq == nullptr || !(max_norm > 0.f)) return DSPARK_ERR_INVALID_ARG;
+  if ((st = check_ws(ws, ws_bytes, clip::ws_bytes(count))) != DSPARK_OK) return st;
+  return cuda_status(clip::launch_scale(tensors, count, sumsq, 0, max_norm, norm, coef, ws,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dspark_status_t dspark_grad_clip(const dspark_tensor_t* tensors, int64_t count, float max_norm, float* norm,
+                                 float* coef, void* ws, size_t ws_bytes, dspark_stream_t stream) {
+  dspark_status_t st = check_tensors(tensors, count, true);
+  if (st != DSPARK_OK) return st;
+  if (!(max_norm > 0.f)) return DSPARK_ERR_INVALID_ARG;
+  if ((st = check_ws(ws, ws_bytes, clip::ws_bytes(count))) != DSPARK_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int64_t n = 0;
+  const cudaError_t e = clip::launch_sumsq(tensors, count, ws, s, &n);
+  if (e != cudaSuccess) return cuda_status(e);
+  return cuda_status(clip::launch_scale(tensors, count, nullptr, n, max_norm, norm, coef, ws, s));
 }
 
 }  // extern "C"

@@ -141,6 +141,11 @@ class Outputs:
         g.accumulate = 1 if accumulate else 0
         return g
 
+    def head_grads(self) -> list:
+        """The head gradients this call writes (dW1, dW2, dconf_w, dconf_b, those present):
+        what a GradClip takes."""
+        return [t for t in (self.dW1, self.dW2, self.dconf_w, self.dconf_b) if t is not None]
+
 
 class Call:
     """A prepared fused forward+backward call: structs built once, launched many times."""
@@ -522,3 +527,115 @@ class LinearCE(_DeviceCall):
             raise ValueError("this call was built without gradients")
         self._run(abi.dspark_lce_bwd, "dspark_lce_bwd", stream, ctypes.byref(self.prob), ctypes.byref(self.grads),
                   self.ws_ptr, self.ws_len)
+
+
+class _EmbedCall(_DeviceCall):
+    def _problem(self, ids, valid, Vt, D, dtype, scale, R):
+        _need(ids, torch.int64, "ids")
+        _need(valid, torch.uint8, "valid")
+        if ids.numel() != R or (valid is not None and valid.numel() != R):
+            raise ValueError(f"ids and valid must hold {R} values")
+        self.device = ids.device
+        _same_device(self.device, valid=valid)
+        p = abi.dspark_embed_problem_t()
+        p.R, p.Vt, p.D, p.dtype = R, Vt, D, _ABI_DTYPE[dtype]
+        p.ids, p.valid, p.scale = _ptr(ids), _ptr(valid), scale
+        self.prob = p
+
+
+class Embedding(_EmbedCall):
+    """A prepared scaled lookup (dspark_embed_fwd): ``out[r] = scale * table[ids[r]]``,
+    zero rows where ``valid`` (uint8) is 0.  ``table`` [Vt, D] is bf16 or fp32 with
+    contiguous rows; ``out`` [ids.numel(), D] has its type (allocated unless given)."""
+
+    def __init__(self, ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0,
+                 valid: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+        self.table_ld = _matrix(table, tuple(_ABI_DTYPE), "table")
+        R, D = ids.numel(), table.shape[1]
+        self._problem(ids, valid, table.shape[0], D, table.dtype, scale, R)
+        self.out = torch.empty(R, D, dtype=table.dtype, device=self.device) if out is None else out
+        out_ld = _matrix(self.out, (table.dtype,), "out")
+        if tuple(self.out.shape) != (R, D):
+            raise ValueError(f"out must be [{R}, {D}]")
+        _same_device(self.device, table=table, out=self.out)
+        self._keep = (ids, valid, table)
+        self._workspace(int(abi.dspark_embed_workspace_size(ctypes.byref(self.prob), 0)))
+        self._args = (ctypes.byref(self.prob), _ptr(table), self.table_ld, _ptr(self.out), out_ld, self.ws_ptr,
+                      self.ws_len)
+
+    def launch(self, stream=None) -> None:
+        self._run(abi.dspark_embed_fwd, "dspark_embed_fwd", stream, *self._args)
+
+
+class EmbeddingGrad(_EmbedCall):
+    """A prepared table gradient (dspark_embed_bwd): ``out[i] = scale * sum of the rows of
+    dout whose id is i``, in row order, every other row zero; with ``accumulate`` (fp32)
+    added to ``out``.  ``dout`` [ids.numel(), D] is bf16 or fp32 with contiguous rows;
+    ``out`` [vocab, D] of type ``dtype`` is allocated unless given."""
+
+    def __init__(self, ids: torch.Tensor, dout: torch.Tensor, vocab: int, scale: float = 1.0,
+                 valid: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.float32,
+                 out: Optional[torch.Tensor] = None, accumulate: bool = False):
+        dout_ld = _matrix(dout, tuple(_ABI_DTYPE), "dout")
+        R, D = dout.shape
+        self._problem(ids, valid, vocab, D, dout.dtype, scale, R)
+        if out is None:
+            out = (torch.zeros if accumulate else torch.empty)(vocab, D, dtype=dtype, device=self.device)
+        self.out = out
+        out_ld = _matrix(out, tuple(_ABI_DTYPE), "out")
+        if tuple(out.shape) != (vocab, D):
+            raise ValueError(f"out must be [{vocab}, {D}]")
+        _same_device(self.device, dout=dout, out=out)
+        self._keep = (ids, valid, dout)
+        self._workspace(int(abi.dspark_embed_workspace_size(ctypes.byref(self.prob), 1)))
+        self._args = (ctypes.byref(self.prob), _ptr(dout), dout_ld, _ptr(out), out_ld, _ABI_DTYPE[out.dtype],
+                      1 if accumulate else 0, self.ws_ptr, self.ws_len)
+
+    def launch(self, stream=None) -> None:
+        self._run(abi.dspark_embed_bwd, "dspark_embed_bwd", stream, *self._args)
+
+
+class GradClip(_DeviceCall):
+    """A prepared clipping of many gradients by their global norm (dspark_grad_clip; with
+    ``group`` dspark_grad_sumsq, an all-reduce of its FP64 sum over that process group, and
+    dspark_grad_scale).  ``grads`` are contiguous bf16 or fp32 tensors; the clipped values
+    go to ``outs`` (same types and sizes) or back into ``grads``.  launch() writes ``norm``
+    and ``coef``."""
+
+    def __init__(self, grads, max_norm: float, outs=None, group=None):
+        grads = list(grads)
+        outs = grads if outs is None else list(outs)
+        if not grads or len(outs) != len(grads):
+            raise ValueError("grads must hold at least one tensor, and outs as many")
+        self.device = grads[0].device
+        arr = (abi.dspark_tensor_t * len(grads))()
+        seen = set()
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            if g.dtype not in _ABI_DTYPE or o.dtype != g.dtype or o.numel() != g.numel():
+                raise ValueError(f"grads[{i}] must be bf16 or fp32, and outs[{i}] like it")
+            _need(g, g.dtype, f"grads[{i}]")
+            _need(o, g.dtype, f"outs[{i}]")
+            _same_device(self.device, **{f"grads[{i}]": g, f"outs[{i}]": o})
+            if g.numel() and g.data_ptr() in seen:
+                raise ValueError(f"grads[{i}] is listed twice")
+            seen.add(g.data_ptr())
+            arr[i] = abi.dspark_tensor_t(g.data_ptr(), o.data_ptr(), g.numel(), _ABI_DTYPE[g.dtype])
+        self.tensors, self.count, self.max_norm, self.group = arr, len(grads), float(max_norm), group
+        self.grads, self.outs = grads, outs
+        self.norm = torch.zeros(1, dtype=torch.float32, device=self.device)
+        self.coef = torch.ones(1, dtype=torch.float32, device=self.device)
+        self.sumsq = torch.zeros(1, dtype=torch.float64, device=self.device)
+        self._workspace(int(abi.dspark_grad_workspace_size(self.count)))
+
+    def launch(self, stream=None) -> None:
+        tail = (self.max_norm, _ptr(self.norm), _ptr(self.coef), self.ws_ptr, self.ws_len)
+        if self.group is None:
+            self._run(abi.dspark_grad_clip, "dspark_grad_clip", stream, self.tensors, self.count, *tail)
+            return
+        import torch.distributed as dist
+        if stream is not None:
+            raise ValueError("with a process group the call runs on the current stream")
+        self._run(abi.dspark_grad_sumsq, "dspark_grad_sumsq", None, self.tensors, self.count, _ptr(self.sumsq),
+                  self.ws_ptr, self.ws_len)
+        dist.all_reduce(self.sumsq, op=dist.ReduceOp.SUM, group=self.group)
+        self._run(abi.dspark_grad_scale, "dspark_grad_scale", None, self.tensors, self.count, _ptr(self.sumsq), *tail)

@@ -1,0 +1,536 @@
+"""The training-step operators on the GPU against their FP64 statements (oracle/train_ops.py).
+
+Bounds, derived before the first run (u = eps / 2 of a type, the largest relative error of
+one rounding: bf16 2^-8, fp32 2^-24):
+
+logits   The tensor cores add sixteen products at a time to an FP32 accumulator, rounding
+         towards zero: at most 2^-23 of the magnitudes added per step, 32 steps a segment of
+         512, and the segments added to nearest.  |error of z| <= E = (32 + H / 512 + 2)
+         2^-23 reach, reach = the largest sum_k |h_k w_k|.
+lse      within E, the 2^-21 of the exponentials, their sum and the logarithm, and the
+         rounding of the value itself: E + 2^-20 + 2^-22 |lse|.  CE: E more.
+dz       relative: 2 E' + 2^-20 of the probabilities (E' = the unsegmented product's error,
+         (H / 16 + 2) 2^-23 reach, against lse's E), and u(bf16) of the rounding.
+dhidden  the relative error of dz times sum |dz w|, the accumulation ((n / 16 + 2) 2^-23 of the
+dweight  same, n the contracted length), and u of the result's own rounding.
+"""
+
+import pytest
+import torch
+
+from oracle import train_ops as O
+
+pytestmark = pytest.mark.gpu
+
+U16, U32 = 2.0 ** -8, 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def T():
+    from speculative_decoding_draft_vocab_b200 import build as _build
+    _build.build()
+    from speculative_decoding_draft_vocab_b200 import torch_api
+    return torch_api
+
+
+def _u(dtype):
+    return U16 if dtype == torch.bfloat16 else U32
+
+
+# ------------------------------------------------------------- linear cross entropy
+def lce_inputs(R, V, H, ignored=0, seed=0, std=3.0, hidden_pad=0, weight_pad=0):
+    g = torch.Generator(device="cuda").manual_seed(1000 + seed)
+    hidden = torch.randn(R, H + hidden_pad, generator=g, device="cuda").to(torch.bfloat16)[:, :H]
+    weight = (torch.randn(V, H + weight_pad, generator=g, device="cuda") * (std / H ** 0.5)).to(torch.bfloat16)[:, :H]
+    targets = torch.randint(0, V, (R,), generator=g, device="cuda")
+    targets[torch.randperm(R, generator=g, device="cuda")[:ignored]] = -100
+    row_weight = torch.rand(R, generator=g, device="cuda") + 0.1
+    return hidden, weight, targets, row_weight
+
+
+def lce_compare(call, ref, H, V, g=1.0, base=None):
+    R = call.ce_rows.numel()
+    E = (32 + H / 512 + 2) * 2.0 ** -23 * ref["reach"]
+    assert int(call.num_tokens) == ref["num_tokens"]
+    lse, ce = call.lse_rows.double(), call.ce_rows.double()
+    tol = E + 2.0 ** -20 + 2.0 ** -22 * ref["lse_rows"].abs()
+    assert bool(((lse - ref["lse_rows"]).abs() <= tol).all())
+    assert bool(((ce - ref["ce_rows"]).abs() <= tol + E).all())
+    dead = ref["lse_rows"] == 0
+    assert bool((lse[dead] == 0).all()) and bool((ce[dead] == 0).all())
+    if call.grads is None:
+        return
+    rel = 2 * ((H / 16 + 2) * 2.0 ** -23 * ref["reach"] + E) + 2.0 ** -20 + U16
+    if call.dhidden is not None:
+        want, mag = ref["dhidden"], ref["dh_mag"]
+        tol = (rel + (V / 16 + 2) * 2.0 ** -23) * mag + U16 * want.abs()
+        assert bool(((call.dhidden.double() - want).abs() <= tol * 1.01).all())
+        none = call.dhidden[mag.sum(1) == 0]
+        assert bool((none == 0).all())
+    if call.dweight is not None:
+        want, mag = ref["dweight"], ref["dw_mag"]
+        got = call.dweight.double() - (0 if base is None else base.double())
+        tol = (rel + (R / 16 + 2) * 2.0 ** -23) * mag + _u(call.dweight.dtype) * want.abs()
+        if base is not None:
+            tol = tol + U32 * (base.double().abs() + want.abs())
+        assert bool(((got - want).abs() <= tol * 1.01).all())
+
+
+@pytest.mark.parametrize("R,V,H,ignored", [
+    (1, 1, 8, 0), (1, 500, 64, 0), (1, 7, 8, 1), (3, 33, 16, 1),
+    (7, 8192, 512, 0), (56, 8192, 512, 9), (64, 257, 72, 0), (65, 255, 136, 1),
+    (127, 1000, 200, 3), (128, 1024, 128, 0), (129, 1025, 520, 2), (130, 700, 72, 130),
+    (255, 3001, 264, 100), (256, 2048, 256, 0), (257, 777, 1032, 5), (448, 5000, 1024, 205),
+    (1021, 4003, 1000, 100), (2049, 769, 328, 1000),
+])
+@pytest.mark.parametrize("z_alpha", [0.0, 1e-3])
+def test_linear_ce_matches_the_statement(T, R, V, H, ignored, z_alpha):
+    h, w, t, a = lce_inputs(R, V, H, ignored, seed=R + V)
+    call = T.LinearCE(h, w, t, row_weight=a, z_alpha=z_alpha)
+    call.grad_scale.fill_(0.75)
+    call.forward()
+    call.backward()
+    assert call.check_status() == 0
+    ref = O.linear_ce(h, w, t, a, z_alpha=z_alpha, grad_scale=0.75)
+    lce_compare(call, ref, H, V)
+    n = max(ref["num_tokens"], 1)
+    E = (32 + H / 512 + 2) * 2.0 ** -23 * ref["reach"]
+    lse = float(ref["lse_rows"].abs().max())
+    tol = n * 1.1 * (2 * E + 2.0 ** -19 + z_alpha * 2 * lse * (E + 2.0 ** -20)) + 2.0 ** -21 * float(
+        (a * ref["ce_rows"].abs()).sum() + z_alpha * (a * ref["lse_rows"] ** 2).sum())
+    assert abs(float(call.loss_num) - float(ref["loss_num"])) <= tol
+
+
+def test_linear_ce_over_several_pieces(T):
+    """More rows and columns than one piece of dz holds (256 MiB): the hidden gradient is
+    added up over the pieces, and the last piece is short."""
+    R, V, H = 8192, 20011, 64
+    h, w, t, a = lce_inputs(R, V, H, 500, seed=1)
+    call = T.LinearCE(h, w, t, row_weight=a, dweight_dtype=torch.float32)
+    call.forward()
+    call.backward()
+    assert call.check_status() == 0
+    lce_compare(call, O.linear_ce(h, w, t, a), H, V)
+
+
+@pytest.mark.parametrize("R", [40, 300])
+def test_linear_ce_strides_scores_and_partial_gradients(T, R):
+    V, H = 1003, 144
+    h, w, t, a = lce_inputs(R, V, H, 7, seed=2, hidden_pad=24, weight_pad=8)
+    ref = O.linear_ce(h, w, t)
+    dh = torch.full((R, H + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    dw = torch.full((V + 1, H + 16), 7.0, dtype=torch.bfloat16, device="cuda")
+    both = T.LinearCE(h, w, t, dhidden=dh[:, :H], dweight=dw[:V, :H])
+    both.forward()
+    both.backward()
+    lce_compare(both, ref, H, V)
+    assert bool((dh[:, H:] == 7).all()) and bool((dw[:, H:] == 7).all()) and bool((dw[V] == 7).all())
+    only_h = T.LinearCE(h, w, t, dweight=False)
+    only_h.forward()
+    only_h.backward()
+    assert torch.equal(only_h.dhidden, dh[:, :H])
+    only_w = T.LinearCE(h, w, t, dhidden=False)
+    only_w.forward()
+    only_w.backward()
+    assert torch.equal(only_w.dweight, dw[:V, :H])
+    score = T.LinearCE(h, w, t, dhidden=False, dweight=False)
+    score.forward()
+    assert torch.equal(score.ce_rows, both.ce_rows) and torch.equal(score.loss_num, both.loss_num)
+    with pytest.raises(ValueError, match="without gradients"):
+        score.backward()
+
+
+@pytest.mark.parametrize("R", [50, 200])
+def test_linear_ce_accumulates_fp32(T, R):
+    V, H = 901, 136
+    h, w, t, a = lce_inputs(R, V, H, 3, seed=3)
+    base = torch.randn(V, H, device="cuda")
+    dw = base.clone()
+    call = T.LinearCE(h, w, t, row_weight=a, dhidden=False, dweight=dw, accumulate=True)
+    call.forward()
+    call.backward()
+    lce_compare(call, O.linear_ce(h, w, t, a), H, V, base=base)
+    # no labelled row: nothing is added
+    none = T.LinearCE(h, w, torch.full_like(t, -100), dhidden=False, dweight=dw, accumulate=True)
+    before = dw.clone()
+    none.forward()
+    none.backward()
+    assert torch.equal(dw, before) and float(none.loss_num) == 0.0
+
+
+def test_linear_ce_rows_without_a_label_are_not_read(T):
+    """NaN and infinities in ignored rows, an id out of range, an ignore_index inside the
+    vocabulary; everything else as without them."""
+    R, V, H = 200, 600, 64
+    h, w, t, a = lce_inputs(R, V, H, 20, seed=4)
+    clean = T.LinearCE(h, w, t)
+    clean.forward()
+    clean.backward()
+    assert clean.check_status() == 0
+    dirty = h.clone()
+    dirty[t == -100] = float("nan")
+    dirty[(t == -100).nonzero()[0]] = float("inf")
+    aw = torch.ones(R, device="cuda")
+    aw[t == -100] = float("nan")
+    call = T.LinearCE(dirty, w, t, row_weight=aw)
+    call.forward()
+    call.backward()
+    for k in ("loss_num", "num_tokens", "ce_rows", "lse_rows", "dhidden", "dweight"):
+        assert torch.equal(getattr(call, k), getattr(clean, k)), k
+    bad = t.clone()
+    bad[t == -100] = V  # out of range: flagged, and no label
+    call = T.LinearCE(dirty, w, bad)
+    call.forward()
+    call.backward()
+    assert call.check_status() == 3  # DSPARK_ERR_ID_OUT_OF_RANGE
+    assert torch.equal(call.dweight, clean.dweight) and torch.equal(call.loss_num, clean.loss_num)
+    inside = torch.where(t == -100, torch.full_like(t, 5), torch.where(t == 5, torch.full_like(t, 6), t))
+    call = T.LinearCE(dirty, w, inside, ignore_index=5)
+    call.forward()
+    call.backward()
+    assert call.check_status() == 0
+    lce_compare(call, O.linear_ce(dirty, w, inside, ignore_index=5), H, V)
+
+
+def test_linear_ce_extreme_logits(T):
+    """Logits of +-1000, where every exponential under- or overflows without the row's own
+    maximum; and a labelled row of NaN, which spoils its own outputs and the sums only."""
+    R, V, H = 140, 515, 8
+    h = torch.zeros(R, H, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(V, H, dtype=torch.bfloat16, device="cuda")
+    h[:, 0] = 1.0
+    h[1::2, 0] = -1.0
+    w[:, 0] = 1000.0
+    w[7, 0] = 1008.0
+    t = torch.arange(R, device="cuda") % V
+    call = T.LinearCE(h, w, t)
+    call.forward()
+    call.backward()
+    lce_compare(call, O.linear_ce(h, w, t), H, V)
+    h[3, 1] = float("nan")
+    call.forward()
+    call.backward()
+    bad = torch.isnan(call.ce_rows)
+    assert bool(bad[3]) and int(bad.sum()) == 1 and bool(torch.isnan(call.loss_num))
+    assert not bool(torch.isnan(call.dhidden[torch.arange(R, device="cuda") != 3]).any())
+
+
+@pytest.mark.parametrize("R,V", [(100, 4000), (600, 9000)])
+def test_linear_ce_repeats_replays_and_keeps_to_its_stream(T, R, V):
+    H = 256
+    h, w, t, a = lce_inputs(R, V, H, 11, seed=5)
+    call = T.LinearCE(h, w, t, row_weight=a)
+    keys = ("loss_num", "num_tokens", "ce_rows", "lse_rows", "dhidden", "dweight")
+
+    def snap():
+        return [getattr(call, k).clone() for k in keys]
+    call.forward()
+    call.backward()
+    call.backward()  # again after one forward
+    first = snap()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call.forward()
+        call.backward()
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(first, snap()))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call.forward()
+        call.backward()
+    h2, _, t2, _ = lce_inputs(R, V, H, 60, seed=6)
+    h.copy_(h2)
+    t.copy_(t2)  # the same buffers, other rows without a label
+    g.replay()
+    replayed = snap()
+    call.forward()
+    call.backward()
+    assert all(torch.equal(x, y) for x, y in zip(replayed, snap()))
+    lce_compare(call, O.linear_ce(h, w, t, a), H, V)
+
+
+def test_linear_ce_gradient_against_differences(T):
+    """The kernels' own loss, moved along a direction, against their gradient: hidden rows
+    are perturbed in exact bf16 steps."""
+    R, V, H = 96, 400, 64
+    h, w, t, a = lce_inputs(R, V, H, 5, seed=7)
+    call = T.LinearCE(h, w, t, row_weight=a, z_alpha=1e-3)
+    call.forward()
+    call.backward()
+    ref = O.linear_ce(h, w, t, a, z_alpha=1e-3)
+    d = torch.zeros(R, H, device="cuda", dtype=torch.float64)
+    d[:, :] = ref["dhidden"].sign()
+    step = 2.0 ** -6
+    losses = []
+    for s in (+1, -1):
+        hs = (h.double() + s * step * d).to(torch.bfloat16)
+        c = T.LinearCE(hs, w, t, row_weight=a, z_alpha=1e-3, dhidden=False, dweight=False)
+        c.forward()
+        losses.append((float(c.loss_num), hs))
+    moved = losses[0][1].double() - losses[1][1].double()  # what the rounding left of the step
+    want = float((call.dhidden.double() * moved).sum())
+    # second-order terms cancel between the two sides but for the rounding of h; third order
+    # and that: a hundredth of the change at this step
+    assert abs((losses[0][0] - losses[1][0]) - want) <= 0.02 * abs(want)
+
+
+# ----------------------------------------------------------------------- embedding
+def _ids(R, Vt, hot, g):
+    ids = torch.randint(0, Vt, (R,), generator=g, device="cuda")
+    if hot:
+        ids[torch.rand(R, generator=g, device="cuda") < hot] = Vt // 2
+    return ids
+
+
+EMB = [(1, 1, 8), (1, 100, 64), (5, 3, 8), (33, 50, 24), (448, 5000, 264), (1000, 7, 512), (4096, 4097, 128),
+       (4097, 100000, 32), (9001, 600, 1032)]
+
+
+@pytest.mark.parametrize("R,Vt,D", EMB)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_embedding_matches_the_statement(T, R, Vt, D, dtype):
+    g = torch.Generator(device="cuda").manual_seed(R + D)
+    table = torch.randn(Vt, D + 8, generator=g, device="cuda").to(dtype)[:, :D]
+    ids = _ids(R, Vt, 0.3, g)
+    valid = (torch.rand(R, generator=g, device="cuda") < 0.8).to(torch.uint8)
+    ids[valid == 0] = -7  # not looked at
+    out = torch.full((R, D + 16), 3.0, dtype=dtype, device="cuda")
+    call = T.Embedding(ids, table, scale=D ** 0.5, valid=valid, out=out[:, :D])
+    call.launch()
+    assert call.check_status() == 0
+    ref = O.embed(ids, table, float(torch.tensor(D ** 0.5, dtype=torch.float32)), valid)
+    # the product in FP32, then the type's rounding
+    assert bool(((out[:, :D].double() - ref).abs() <= (U32 + _u(dtype)) * 1.01 * ref.abs()).all())
+    assert bool((out[:, D:] == 3.0).all())
+    ids[0] = Vt
+    valid[0] = 1
+    call.launch()
+    assert call.check_status() == 3 and bool((out[0, :D] == 0).all())
+
+
+@pytest.mark.parametrize("R,Vt,D", EMB + [(40000, 11, 64), (70001, 151936, 16)])
+@pytest.mark.parametrize("dtype,grad", [(torch.bfloat16, torch.float32), (torch.bfloat16, torch.bfloat16),
+                                        (torch.float32, torch.float32), (torch.float32, torch.bfloat16)])
+@pytest.mark.parametrize("hot", [0.0, 0.4])
+def test_embedding_gradient_matches_the_statement(T, R, Vt, D, dtype, grad, hot):
+    g = torch.Generator(device="cuda").manual_seed(R + D + 1)
+    dout = torch.randn(R, D + 8, generator=g, device="cuda").to(dtype)[:, :D]
+    ids = _ids(R, Vt, hot, g)
+    valid = (torch.rand(R, generator=g, device="cuda") < 0.8).to(torch.uint8)
+    ids[valid == 0] = 1 << 40
+    dout[valid == 0] = float("nan")  # not read
+    buf = torch.full((Vt, D + 8), 5.0, dtype=grad, device="cuda")
+    call = T.EmbeddingGrad(ids, dout, Vt, scale=1.5, valid=valid, out=buf[:, :D])
+    call.launch()
+    assert call.check_status() == 0
+    ref, mag, n = O.embed_grad(ids, dout, Vt, 1.5, valid)
+    # n additions in FP32 and the scale's rounding, then the type's
+    tol = (n[:, None] + 2) * U32 * mag + _u(grad) * ref.abs()
+    assert bool(((buf[:, :D].double() - ref).abs() <= tol * 1.01).all())
+    assert bool((buf[:, :D][n == 0] == 0).all()) and bool((buf[:, D:] == 5.0).all())
+    first = buf.clone()
+    call.launch()
+    assert torch.equal(buf, first)
+
+
+@pytest.mark.parametrize("R,Vt,D", [(1, 9, 8), (500, 40, 136), (9001, 600, 64)])
+def test_embedding_gradient_accumulates(T, R, Vt, D):
+    g = torch.Generator(device="cuda").manual_seed(R)
+    dout = torch.randn(R, D, generator=g, device="cuda").to(torch.bfloat16)
+    ids = _ids(R, Vt, 0.2, g)
+    ids[ids == 3] = 4  # a row that nothing is added to
+    base = torch.randn(Vt, D, generator=g, device="cuda")
+    base[3] = float("nan")
+    table = base.clone()
+    call = T.EmbeddingGrad(ids, dout, Vt, out=table, accumulate=True)
+    call.launch()
+    ref, mag, n = O.embed_grad(ids, dout, Vt)
+    on = torch.arange(Vt, device="cuda") != 3
+    tol = (n[:, None] + 2) * U32 * mag + U32 * (base.double().abs() + mag)
+    assert bool(((table.double() - base.double() - ref).abs() <= tol * 1.01)[on].all())
+    assert bool(torch.isnan(table[3]).all())  # left as it was
+    with pytest.raises(Exception, match="not supported"):
+        T.EmbeddingGrad(ids, dout, Vt, dtype=torch.bfloat16, accumulate=True).launch()
+
+
+def test_embedding_gradient_edges(T):
+    """Nothing valid; every row the same id; an id out of range; a replayed capture."""
+    R, Vt, D = 5000, 64, 40
+    dout = torch.randn(R, D, device="cuda")
+    ids = torch.full((R,), 63, device="cuda")
+    call = T.EmbeddingGrad(ids, dout, Vt, valid=torch.zeros(R, dtype=torch.uint8, device="cuda"))
+    call.launch()
+    assert call.check_status() == 0 and not bool(call.out.any())
+    call = T.EmbeddingGrad(ids, dout, Vt)
+    call.launch()
+    ref, mag, n = O.embed_grad(ids, dout, Vt)
+    assert bool(((call.out.double() - ref).abs() <= 1.01 * (n[:, None] + 2) * U32 * mag).all())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call.launch()
+    ids.copy_(torch.randint(0, Vt, (R,), device="cuda"))
+    ids[17] = -1
+    graph.replay()
+    assert call.check_status() == 3
+    ref, mag, n = O.embed_grad(ids, dout, Vt)
+    assert bool(((call.out.double() - ref).abs() <= 1.01 * (n[:, None] + 2) * U32 * mag).all())
+
+
+# ------------------------------------------------------------------------ clipping
+def _flat(sizes, dtype, off, scale=1.0, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    buf = (torch.randn(sum(sizes) + off + 8, generator=g, device="cuda") * scale).to(dtype)
+    out, at = [], off
+    for n in sizes:
+        out.append(buf[at:at + n])
+        at += n
+    return buf, out
+
+
+SIZES = [[1], [0, 5, 0], [8191, 8192, 8193], [1, 2, 3, 5, 7, 100001, 13], [17] * 700, [3000001]]
+
+
+@pytest.mark.parametrize("sizes", SIZES, ids=lambda s: f"{len(s)}x{max(s)}")
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("off", [0, 3])
+@pytest.mark.parametrize("factor", [0.3, 4.0])
+def test_clip_matches_the_statement(T, sizes, dtype, off, factor):
+    buf, grads = _flat(sizes, dtype, off, seed=len(sizes))
+    max_norm = factor * float(torch.cat([g.double() for g in grads]).norm())
+    norm, coef, want = O.clip(grads, max_norm)
+    dst, outs = _flat(sizes, dtype, off + 1 if factor < 1 else off, seed=9)
+    for into in (outs, None):  # to buffers that meet 16 bytes elsewhere, then in place
+        call = T.GradClip(grads, max_norm, outs=into)
+        edges = [buf[:off].clone(), buf[off + sum(sizes):].clone()]
+        call.launch()
+        assert call.check_status() == 0
+        # FP64 sums of squares each right to 2^-22, one square root and three FP32 roundings
+        assert abs(float(call.norm) - norm) <= 2.0 ** -21 * norm
+        assert abs(float(call.coef) - coef) <= 2.0 ** -20 * coef
+        for g, w in zip(call.outs, want):
+            assert bool(((g.double() - w).abs() <= (2.0 ** -20 + 1.01 * _u(dtype)) * w.abs() + 1e-45).all())
+        assert torch.equal(buf[:off], edges[0]) and torch.equal(buf[off + sum(sizes):], edges[1])
+
+
+def test_clip_values_out_of_the_ordinary(T):
+    big = torch.full((1000,), 1e25, device="cuda")      # squares overflow FP32
+    small = torch.full((1000,), 1e-25, device="cuda")   # and underflow
+    zero = torch.zeros(5000, device="cuda")
+    for g in (big, small, zero):
+        norm, coef, want = O.clip([g], 1.0)
+        call = T.GradClip([g.clone()], 1.0)
+        call.launch()
+        assert abs(float(call.norm) - norm) <= 2.0 ** -21 * norm
+        assert bool(((call.outs[0].double() - want[0]).abs() <= 2.0 ** -19 * want[0].abs()).all())
+    for bad in (float("inf"), float("nan")):
+        g = torch.randn(3001, device="cuda")
+        g[1234] = bad
+        before = g.clone()
+        out = torch.empty_like(g)
+        call = T.GradClip([g], 0.5, outs=[out])
+        call.launch()
+        assert not bool(torch.isfinite(call.norm)) and float(call.coef) == 1.0
+        assert torch.equal(torch.nan_to_num(out, 9.0, 8.0), torch.nan_to_num(before, 9.0, 8.0))
+
+
+def test_clip_repeats_and_replays(T):
+    _, grads = _flat([100003, 77, 4096 * 5], torch.float32, 1, seed=3)
+    _, more = _flat([60001, 12], torch.bfloat16, 1, seed=4)
+    grads = grads + more
+    outs = [torch.empty_like(g) for g in grads]
+    call = T.GradClip(grads, 3.0, outs=outs)
+    call.launch()
+    first = [o.clone() for o in outs] + [call.norm.clone()]
+    call.launch()
+    assert all(torch.equal(x, y) for x, y in zip(first, outs + [call.norm]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call.launch()
+    for g in grads:
+        g.mul_(-2.0)
+    graph.replay()
+    norm, coef, want = O.clip(grads, 3.0)
+    assert abs(float(call.norm) - norm) <= 2.0 ** -21 * norm
+    for g, w in zip(outs, want):
+        assert bool(((g.double() - w).abs() <= (2.0 ** -20 + 1.01 * _u(g.dtype)) * w.abs()).all())
+    with pytest.raises(ValueError, match="twice"):
+        T.GradClip([grads[0], grads[0]], 1.0)
+
+
+def test_clip_in_two_steps(T):
+    """dspark_grad_sumsq and dspark_grad_scale, as ranks use them around an all-reduce: two
+    halves of a gradient clipped by the norm of the whole equal the whole clipped at once."""
+    import ctypes
+    from speculative_decoding_draft_vocab_b200 import abi
+    g = torch.randn(50000, device="cuda")
+    whole = T.GradClip([g], 2.0, outs=[torch.empty_like(g)])
+    whole.launch()
+    halves = [T.GradClip([h], 2.0, outs=[torch.empty_like(h)]) for h in (g[:30000], g[30000:])]
+    s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    for h in halves:
+        abi.check(abi.dspark_grad_sumsq(h.tensors, 1, h.sumsq.data_ptr(), h.ws_ptr, h.ws_len, s), "sumsq")
+    total = halves[0].sumsq + halves[1].sumsq
+    for h in halves:
+        abi.check(abi.dspark_grad_scale(h.tensors, 1, total.data_ptr(), 2.0, h.norm.data_ptr(), h.coef.data_ptr(),
+                                        h.ws_ptr, h.ws_len, s), "scale")
+        assert h.check_status() == 0
+        assert abs(float(h.norm) - float(whole.norm)) <= 2.0 ** -22 * float(whole.norm)
+    both = torch.cat([h.outs[0] for h in halves])
+    assert bool(((both - whole.outs[0]).abs() <= 2.0 ** -21 * whole.outs[0].abs()).all())
+
+
+# ------------------------------------------------------------------ used together
+def test_a_training_step_of_all_of_them(T):
+    """Tokens -> scaled embedding -> linear cross entropy with a tied head -> both gradients
+    of the table in one FP32 buffer -> clipping; against the same chain in FP64 from the
+    kernels' own bf16 activations.  Then the heads' gradients of the fused loss, clipped."""
+    from speculative_decoding_draft_vocab_b200.synthetic import make_inputs
+    R, V, H, scale = 300, 2003, 128, 2.0
+    g = torch.Generator(device="cuda").manual_seed(8)
+    table = (torch.randn(V, H, generator=g, device="cuda") * 0.2).to(torch.bfloat16)
+    ids = _ids(R, V, 0.2, g)
+    targets = torch.roll(ids, -1)
+    targets[-1] = -100
+    emb = T.Embedding(ids, table, scale=scale)
+    emb.launch()
+    dtable = torch.empty(V, H, device="cuda")
+    ce = T.LinearCE(emb.out, table, targets, dweight=dtable, accumulate=False)
+    ce.forward()
+    ce.backward()
+    back = T.EmbeddingGrad(ids, ce.dhidden, V, scale=scale, out=dtable, accumulate=True)
+    back.launch()
+    clip = T.GradClip([dtable], 0.5)
+    head = dtable.clone()
+    clip.launch()
+    torch.cuda.synchronize()
+    assert emb.check_status() == ce.check_status() == back.check_status() == clip.check_status() == 0
+    ref = O.linear_ce(emb.out, table, targets)
+    lce_compare(T_no_weight(ce), ref, H, V)
+    want, mag, n = O.embed_grad(ids, ce.dhidden, V, scale)
+    want = want + ref["dweight"]
+    rel = 2 * ((H / 16 + 2) + (32 + H / 512 + 2)) * 2.0 ** -23 * ref["reach"] + 2.0 ** -20 + U16
+    tol = (rel + (R / 16 + 2) * 2.0 ** -23) * ref["dw_mag"] + (n[:, None] + 4) * U32 * (mag + ref["dw_mag"])
+    assert bool(((head.double() - want).abs() <= 1.01 * tol).all())
+    norm, coef, clipped = O.clip([head], 0.5)
+    assert abs(float(clip.norm) - norm) <= 2.0 ** -21 * norm and coef < 1.0
+    assert bool(((dtable.double() - clipped[0]).abs() <= 2.0 ** -19 * clipped[0].abs()).all())
+
+    inp = make_inputs("recipe_heads", device="cuda", B=1, N=3, K=7, V=2048, hidden=256, rank=64, seed=3)
+    out = T.dspark_loss(inp)
+    grads = out.head_grads()
+    assert len(grads) == 4
+    norm, coef, clipped = O.clip(grads, 0.1)
+    call = T.GradClip(grads, 0.1)
+    call.launch()
+    assert abs(float(call.norm) - norm) <= 2.0 ** -21 * norm
+    for got, w in zip(grads, clipped):
+        assert bool(((got.double() - w).abs() <= 2.0 ** -19 * w.abs()).all())
+
+
+def T_no_weight(call):
+    """`call` with its weight gradient set aside (another kernel added to that buffer)."""
+    import copy
+    c = copy.copy(call)
+    c.dweight = None
+    return c
