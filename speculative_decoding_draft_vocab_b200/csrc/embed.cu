@@ -49,11 +49,22 @@ __device__ __forceinline__ bool dropped(const dspark_embed_problem_t& p, int64_t
 __device__ __forceinline__ bool in_table(const dspark_embed_problem_t& p, int64_t id) { return id >= 0 && id < p.Vt; }
 
 // Whether any row that counts has an id outside the table; by one CTA, which also makes the
-// status word this call's.
+// status word this call's.  Sixteen rows per thread in flight.
 __device__ void check_ids(const dspark_embed_problem_t& p, WsEmbedHeader* hdr) {
+  constexpr int U = 16;
   int bad = 0;
-  for (int64_t r = threadIdx.x; r < p.R; r += blockDim.x)
-    if (!dropped(p, r) && !in_table(p, p.ids[r])) bad = 1;
+  for (int64_t r0 = threadIdx.x; r0 < p.R; r0 += U * blockDim.x) {
+    int64_t id[U];
+    uint8_t on[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = r0 + u * blockDim.x;
+      id[u] = r < p.R ? p.ids[r] : 0;
+      on[u] = p.valid && r < p.R ? p.valid[r] : 1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) bad |= on[u] && !in_table(p, id[u]);
+  }
   bad = __syncthreads_or(bad);
   if (threadIdx.x == 0) hdr->status = bad ? kFlagIdOutOfRange : 0u;
 }
@@ -98,53 +109,246 @@ __global__ void __launch_bounds__(256) lookup_kernel(const FwdArgs a) {
   }
 }
 
+// ------------------------------------------------------------------ zero rows
+// The table rows that no id touches.  While the ids are sorted, what is touched is not known
+// and the memory is idle: the sorting kernels' spare CTAs zero the first plan.fill rows
+// whatever their ids (a touched one is written again later); the two kernels after the sort
+// zero the others beside their sums, looking each row up in the sorted keys.
+template <bool TF32>
+__device__ void zero_rows(const BwdArgs& a, int64_t r0, int64_t r1, int64_t thread, int64_t threads) {
+  constexpr int N = Vec<TF32>::N;
+  const int64_t nv = a.p.D / N, ldv = a.dtable_ld / N;
+  uint4* t = static_cast<uint4*>(a.dtable);
+  if (ldv == nv) {
+    for (int64_t i = r0 * nv + thread; i < r1 * nv; i += threads) t[i] = make_uint4(0u, 0u, 0u, 0u);
+  } else {
+    for (int64_t i = thread; i < (r1 - r0) * nv; i += threads) {
+      const int64_t r = i / nv;
+      t[(r0 + r) * ldv + (i - r * nv)] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+}
+
+// CTA `cta` of `ctas` zeroes its share of part `part` of `parts` of the first plan.fill rows.
+__device__ __forceinline__ void zero_share(const BwdArgs& a, int part, int parts, int cta, int ctas) {
+  const int64_t r0 = a.plan.fill * part / parts, r1 = a.plan.fill * (part + 1) / parts;
+  const int64_t thread = int64_t(cta) * blockDim.x + threadIdx.x, threads = int64_t(ctas) * blockDim.x;
+  if (a.table_f32) zero_rows<true>(a, r0, r1, thread, threads);
+  else zero_rows<false>(a, r0, r1, thread, threads);
+}
+
 // ------------------------------------------------------------------ sort
-// One radix pass over digit [shift, shift + kDigitBits) is two kernels: each CTA counts the
-// digits of its run of rows; then each CTA finds where its rows of each digit go (all
-// smaller digits, the same digit in the CTAs before it) and moves them in order.  The first
-// pass reads the ids themselves.
+// Keys are the ids, Vt for rows that do not count; 9-bit digits, least first.  Ranks within a
+// warp come from ballots, in row order, so every pass is stable.
+__device__ __forceinline__ uint32_t key_of(const BwdArgs& a, int64_t i, bool& bad) {
+  const int64_t id = a.p.ids[i];
+  if (dropped(a.p, i)) return uint32_t(a.p.Vt);
+  if (in_table(a.p, id)) return uint32_t(id);
+  bad = true;
+  return uint32_t(a.p.Vt);
+}
+
+// Ranks of a warp's items among the earlier ones of the same digit; `cnt`: its digit counts.
+template <int ITEMS>
+__device__ __forceinline__ void warp_ranks(const uint32_t (&digit)[ITEMS], uint16_t* cnt, uint32_t (&rank)[ITEMS],
+                                           int lane) {
+  for (int d = lane; d < kDigits / 2; d += 32) reinterpret_cast<uint32_t*>(cnt)[d] = 0;
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    uint32_t same = 0xffffffffu;  // the lanes with this digit, bit by bit
+#pragma unroll
+    for (int b = 0; b <= kDigitBits; ++b) {
+      const bool one = (digit[k] >> b) & 1u;
+      const uint32_t m = __ballot_sync(0xffffffffu, one);
+      same &= one ? m : ~m;
+    }
+    const bool on = digit[k] < kDigits;
+    if (on) rank[k] = cnt[digit[k]] + __popc(same & ((1u << lane) - 1u));
+    __syncwarp();
+    if (on && lane == __ffs(same) - 1) cnt[digit[k]] += uint16_t(__popc(same));
+    __syncwarp();
+  }
+}
+
+// Up to kSmallRows rows: one cluster of eight CTAs keeps them in registers, one, two or four
+// per thread, and moves them through its distributed shared memory; the other clusters zero
+// table rows meanwhile.  (8192 rows: 20 us in one CTA, whose issue slots the ranking fills.)
+struct SmallSort {
+  uint64_t item[kSmallThreads * kSmallItems];  // key, row: one remote store each
+  uint16_t cnt[kSmallThreads / 32][kDigits];
+  uint32_t mine[kDigits];  // digit counts of this CTA, read by the others
+  uint32_t wsum[kSmallThreads / 32];
+  uint32_t bad;
+};
+
+__device__ __forceinline__ uint32_t ld_dsmem(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int ITEMS>
+__global__ void __launch_bounds__(kSmallThreads) small_sort_kernel(const BwdArgs a) {
+  pdl_trigger();
+  if (blockIdx.x >= kSmallCtas) {  // whole clusters
+    zero_share(a, 0, 1, int(blockIdx.x) - kSmallCtas, int(gridDim.x) - kSmallCtas);
+    return;
+  }
+  extern __shared__ uint4 smem_small[];
+  SmallSort& sm = *reinterpret_cast<SmallSort*>(smem_small);
+  constexpr int kWarps = kSmallThreads / 32, CAP = kSmallThreads * ITEMS;  // rows per CTA
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cta = int(cluster_ctarank());
+  const int l0 = warp * 32 * ITEMS + lane;  // a warp's items are consecutive rows, 32 at a time
+  const int R = int(a.p.R);
+  uint32_t key[ITEMS], row[ITEMS];
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    row[k] = uint32_t(cta * CAP + l0 + 32 * k);
+    key[k] = int(row[k]) < R ? key_of(a, row[k], bad) : ~0u;  // past the rows: last in every pass
+  }
+  const int any_bad = __syncthreads_or(bad);
+  if (tid == 0) sm.bad = any_bad ? kFlagIdOutOfRange : 0u;
+  for (int p = 0; p < a.plan.passes; ++p) {
+    uint32_t digit[ITEMS], rank[ITEMS];
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) digit[k] = (key[k] >> (p * kDigitBits)) & (kDigits - 1);
+    warp_ranks<ITEMS>(digit, sm.cnt[warp], rank, lane);
+    __syncthreads();
+    // two threads per digit, sixteen warps each
+    const int d = tid >> 1, half = tid & 1, w0 = half * (kWarps / 2);
+    uint32_t own = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps / 2; ++w) own += sm.cnt[w0 + w][d];
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+    if (half == 0) sm.mine[d] = own + other;
+    cluster_sync();  // every CTA's counts are there, and its items in registers
+    uint32_t before = 0, total = 0;
+#pragma unroll
+    for (int c = 0; c < kSmallCtas / 2; ++c) {
+      const int from = half * (kSmallCtas / 2) + c;
+      const uint32_t n = ld_dsmem(dsmem_map(smem_u32(&sm.mine[d]), uint32_t(from)));
+      if (from < cta) before += n;
+      total += n;
+    }
+    before += __shfl_xor_sync(0xffffffffu, before, 1);
+    total += __shfl_xor_sync(0xffffffffu, total, 1);
+    uint32_t incl = half ? total : 0u;  // a digit counts once, at its second thread
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 31) sm.wsum[warp] = incl;
+    __syncthreads();
+    uint32_t lower = lane < warp ? sm.wsum[lane] : 0u;
+    lower = __reduce_add_sync(0xffffffffu, lower);
+    uint32_t at = lower + incl - (half ? total : 0u) + before + (half ? other : 0u);
+#pragma unroll
+    for (int w = 0; w < kWarps / 2; ++w) {  // counts become places
+      const uint32_t n = sm.cnt[w0 + w][d];
+      sm.cnt[w0 + w][d] = uint16_t(at);
+      at += n;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const uint32_t to = sm.cnt[warp][digit[k]] + rank[k];
+      const uint32_t there = to / CAP, slot = to % CAP;
+      asm volatile("st.shared::cluster.u64 [%0], %1;"
+                   ::"r"(dsmem_map(smem_u32(&sm.item[slot]), there)), "l"(uint64_t(row[k]) << 32 | key[k]) : "memory");
+    }
+    if (p == 0 && cta == 0 && warp == 0) {  // the call's status from the eight CTAs'
+      uint32_t f = lane < kSmallCtas ? ld_dsmem(dsmem_map(smem_u32(&sm.bad), uint32_t(lane))) : 0u;
+      f = __reduce_or_sync(0xffffffffu, f);
+      if (lane == 0) a.ws.hdr->status = f;
+    }
+    cluster_sync();
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) key[k] = uint32_t(sm.item[l0 + 32 * k]), row[k] = uint32_t(sm.item[l0 + 32 * k] >> 32);
+    // the next pass writes these places only after its first cluster barrier
+  }
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const int i = cta * CAP + l0 + 32 * k;
+    if (i < R) a.ws.key[0][i] = key[k], a.ws.row[0][i] = row[k];
+  }
+}
+
+template <int ITEMS>
+cudaError_t small_sort(const BwdArgs& a, cudaStream_t s) {
+  auto kern = small_sort_kernel<ITEMS>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(SmallSort)));
+  if (e != cudaSuccess) return e;
+  const int spare = a.plan.fill > 0 ? 148 * 2 / kSmallCtas * kSmallCtas : 0;
+  PdlLaunch l(kSmallCtas + spare, kSmallThreads, sizeof(SmallSort), s, kSmallCtas);
+  l.at[0].val.programmaticStreamSerializationAllowed = 0;  // the first kernel of the call waits for all work before it
+  return cudaLaunchKernelEx(&l.cfg, kern, a);
+}
+
+// More rows: a pass is two kernels.  Each CTA counts the digits of its run of rows; then each
+// CTA finds where its rows of each digit go (all smaller digits, the same digit in the CTAs
+// before it) and moves them in order.  The first pass reads the ids themselves.
 struct Pass {
-  int shift, first;
+  int shift, index;
   const uint32_t* key_in;
   const uint32_t* row_in;
   uint32_t* key_out;
   uint32_t* row_out;
 };
 
-__device__ __forceinline__ uint32_t load_key(const BwdArgs& a, const Pass& ps, int64_t i) {
-  if (!ps.first) return ps.key_in[i];
-  const int64_t id = a.p.ids[i];
-  return !dropped(a.p, i) && in_table(a.p, id) ? uint32_t(id) : uint32_t(a.p.Vt);
-}
-
 __global__ void __launch_bounds__(kSortThreads) count_kernel(const BwdArgs a, const Pass ps) {
   pdl_wait();
   pdl_trigger();
-  if (int(blockIdx.x) == a.plan.ctas) {  // first pass only: one CTA more
-    check_ids(a.p, a.ws.hdr);
+  if (int(blockIdx.x) >= a.plan.ctas) {
+    zero_share(a, 2 * ps.index, 2 * a.plan.passes, int(blockIdx.x) - a.plan.ctas, int(gridDim.x) - a.plan.ctas);
     return;
   }
   __shared__ uint32_t c[kDigits];
   for (int d = threadIdx.x; d < kDigits; d += kSortThreads) c[d] = 0;
   __syncthreads();
   const int64_t i0 = int64_t(blockIdx.x) * a.plan.run, i1 = min(i0 + a.plan.run, a.p.R);
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads)
-    atomicAdd(&c[(load_key(a, ps, i) >> ps.shift) & (kDigits - 1)], 1u);
-  __syncthreads();
+  bool bad = false;
+  for (int64_t c0 = i0 + threadIdx.x; c0 < i1; c0 += kSortChunk) {
+    uint32_t key[kSortItems];
+#pragma unroll
+    for (int k = 0; k < kSortItems; ++k) {
+      const int64_t i = c0 + k * kSortThreads;
+      key[k] = i >= i1 ? 0u : ps.index == 0 ? key_of(a, i, bad) : ps.key_in[i];
+    }
+#pragma unroll
+    for (int k = 0; k < kSortItems; ++k)
+      if (c0 + k * kSortThreads < i1) atomicAdd(&c[(key[k] >> ps.shift) & (kDigits - 1)], 1u);
+  }
+  const int any_bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0 && ps.index == 0) a.ws.flags[blockIdx.x] = any_bad ? kFlagIdOutOfRange : 0u;
   for (int d = threadIdx.x; d < kDigits; d += kSortThreads) a.ws.counts[size_t(blockIdx.x) * kDigits + d] = c[d];
 }
 
 __global__ void __launch_bounds__(kSortThreads) move_kernel(const BwdArgs a, const Pass ps) {
   pdl_wait();
   pdl_trigger();
+  if (int(blockIdx.x) >= a.plan.ctas) {
+    zero_share(a, 2 * ps.index + 1, 2 * a.plan.passes, int(blockIdx.x) - a.plan.ctas, int(gridDim.x) - a.plan.ctas);
+    return;
+  }
   static_assert(kSortThreads == kDigits, "one thread per digit");
   constexpr int kWarps = kSortThreads / 32;
   __shared__ uint32_t base[kDigits];
   __shared__ uint16_t cnt[kWarps][kDigits];
   __shared__ uint32_t wsum[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (blockIdx.x == 0 && warp == 0 && ps.index == 0) {  // the call's status from the runs'
+    uint32_t f = 0;
+    for (int c = lane; c < a.plan.ctas; c += 32) f |= a.ws.flags[c];
+    f = __reduce_or_sync(0xffffffffu, f);
+    if (lane == 0) a.ws.hdr->status = f;
+  }
   {  // thread = digit
     uint32_t before = 0, total = 0;
+#pragma unroll 8
     for (int c = 0; c < a.plan.ctas; ++c) {
       const uint32_t n = a.ws.counts[size_t(c) * kDigits + tid];
       if (c < int(blockIdx.x)) before += n;
@@ -164,65 +368,37 @@ __global__ void __launch_bounds__(kSortThreads) move_kernel(const BwdArgs a, con
   }
   const int64_t i0 = int64_t(blockIdx.x) * a.plan.run, i1 = min(i0 + a.plan.run, a.p.R);
   for (int64_t c0 = i0; c0 < i1; c0 += kSortChunk) {
-    for (int d = lane; d < kDigits; d += 32) cnt[warp][d] = 0;
-    __syncwarp();
-    uint32_t key[kSortItems], row[kSortItems], rank[kSortItems];
+    uint32_t key[kSortItems], row[kSortItems], digit[kSortItems], rank[kSortItems];
     // a warp's items are 32 * kSortItems consecutive rows, taken 32 at a time: row order
     const int64_t w0 = c0 + warp * 32 * kSortItems + lane;
+    bool bad = false;
 #pragma unroll
     for (int k = 0; k < kSortItems; ++k) {
       const int64_t i = w0 + 32 * k;
       const bool on = i < i1;
-      key[k] = on ? load_key(a, ps, i) : 0u;
-      row[k] = on ? (ps.first ? uint32_t(i) : ps.row_in[i]) : 0u;
+      key[k] = !on ? 0u : ps.index == 0 ? key_of(a, i, bad) : ps.key_in[i];
+      row[k] = !on ? 0u : ps.index == 0 ? uint32_t(i) : ps.row_in[i];
+      digit[k] = on ? (key[k] >> ps.shift) & (kDigits - 1) : uint32_t(kDigits);
     }
+    warp_ranks<kSortItems>(digit, cnt[warp], rank, lane);
+    __syncthreads();
+    uint32_t at = 0;  // thread = digit: the warps' counts become offsets within the digit
+    for (int w = 0; w < kWarps; ++w) {
+      const uint32_t n = cnt[w][tid];
+      cnt[w][tid] = uint16_t(at);
+      at += n;
+    }
+    __syncthreads();
 #pragma unroll
     for (int k = 0; k < kSortItems; ++k) {
-      const bool on = w0 + 32 * k < i1;
-      const uint32_t d = on ? (key[k] >> ps.shift) & (kDigits - 1) : uint32_t(kDigits);
-      const uint32_t same = __match_any_sync(0xffffffffu, d);
-      const int lead = __ffs(same) - 1;
-      if (on) rank[k] = cnt[warp][d] + __popc(same & ((1u << lane) - 1u));
-      __syncwarp();
-      if (on && lane == lead) cnt[warp][d] += uint16_t(__popc(same));
-      __syncwarp();
+      if (digit[k] == uint32_t(kDigits)) continue;
+      const uint32_t to = base[digit[k]] + cnt[warp][digit[k]] + rank[k];
+      ps.key_out[to] = key[k];
+      ps.row_out[to] = row[k];
     }
     __syncthreads();
-    {  // thread = digit: the warps' counts become offsets within the digit
-      uint32_t at = 0;
-      for (int w = 0; w < kWarps; ++w) {
-        const uint32_t n = cnt[w][tid];
-        cnt[w][tid] = uint16_t(at);
-        at += n;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < kSortItems; ++k) {
-        if (w0 + 32 * k >= i1) continue;
-        const uint32_t d = (key[k] >> ps.shift) & (kDigits - 1);
-        const uint32_t to = base[d] + cnt[warp][d] + rank[k];
-        ps.key_out[to] = key[k];
-        ps.row_out[to] = row[k];
-      }
-      __syncthreads();
-      base[tid] += at;
-    }
+    base[tid] += at;
     __syncthreads();
-  }
-}
-
-// ------------------------------------------------------------------ zero rows
-template <bool TF32>
-__global__ void __launch_bounds__(256) zero_kernel(const BwdArgs a) {
-  pdl_trigger();
-  constexpr int N = Vec<TF32>::N;
-  const int64_t nv = a.p.D / N, total = a.p.Vt * nv, ldv = a.dtable_ld / N;
-  uint4* t = static_cast<uint4*>(a.dtable);
-  if (ldv == nv) {
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) t[i] = make_uint4(0u, 0u, 0u, 0u);
-  } else {
-    for (int64_t r = blockIdx.x; r < a.p.Vt; r += gridDim.x)
-      for (int64_t j = threadIdx.x; j < nv; j += 256) t[r * ldv + j] = make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -234,13 +410,13 @@ __device__ __forceinline__ void write_row(const BwdArgs& a, uint32_t id, int64_t
     float* d = static_cast<float*>(a.dtable) + size_t(id) * a.dtable_ld + col;
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      float4 o = make_float4(acc[i] * a.p.scale, acc[i + 1] * a.p.scale, acc[i + 2] * a.p.scale, acc[i + 3] * a.p.scale);
-      float4* at = reinterpret_cast<float4*>(d + i);
-      if (a.accumulate) {
-        const float4 old = *at;
-        o.x += old.x, o.y += old.y, o.z += old.z, o.w += old.w;
-      }
-      *at = o;
+      const float4 o = make_float4(acc[i] * a.p.scale, acc[i + 1] * a.p.scale, acc[i + 2] * a.p.scale, acc[i + 3] * a.p.scale);
+      // an element gets one addition per call, so its value does not depend on any order;
+      // the reduction does not wait for the old value
+      if (a.accumulate)
+        asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(d + i), "f"(o.x), "f"(o.y), "f"(o.z), "f"(o.w) : "memory");
+      else
+        *reinterpret_cast<float4*>(d + i) = o;
     }
   } else {
     uint16_t* d = static_cast<uint16_t*>(a.dtable) + size_t(id) * a.dtable_ld + col;
@@ -252,7 +428,41 @@ __device__ __forceinline__ void write_row(const BwdArgs& a, uint32_t id, int64_t
   }
 }
 
-// A warp sums one window's rows over 32 vectors of columns.
+// The first of the n sorted keys that is not below `id`; a warp looks at 32 at a time.
+__device__ __forceinline__ int64_t lower_bound(const uint32_t* key, int64_t n, uint32_t id, int lane) {
+  int64_t lo = 0;
+  while (n > 0) {
+    const int64_t step = (n + 31) / 32, at = (lane + 1) * step - 1;
+    const int below = __popc(__ballot_sync(0xffffffffu, at < n && key[lo + at] < id));
+    lo += below * step;
+    n = min(step - 1, n - below * step);  // the probe that was not below is itself a candidate
+  }
+  return lo;
+}
+
+// A warp zeroes those of 32 table rows, from `r0` and below `r1`, that no sorted key names.
+template <bool TF32>
+__device__ void zero_untouched(const BwdArgs& a, const uint32_t* key, int64_t r0, int64_t r1, int lane) {
+  constexpr int N = Vec<TF32>::N;
+  const int64_t nv = a.p.D / N, ldv = a.dtable_ld / N;
+  uint32_t free = r1 - r0 < 32 ? (1u << (r1 - r0)) - 1u : 0xffffffffu;
+  for (uint32_t from = uint32_t(r0);;) {  // again only where more than 32 keys name these rows
+    const int64_t at = lower_bound(key, a.p.R, from, lane) + lane;
+    const uint32_t k = at < a.p.R ? key[at] : ~0u, off = k - uint32_t(r0);
+    free &= ~__reduce_or_sync(0xffffffffu, off < 32u ? 1u << off : 0u);
+    const uint32_t top = __shfl_sync(0xffffffffu, off, 31);
+    if (top >= 31u) break;
+    from = uint32_t(r0) + top + 1;
+  }
+  uint4* t = static_cast<uint4*>(a.dtable);
+  for (uint32_t m = free; m != 0; m &= m - 1) {
+    uint4* d = t + (r0 + __ffs(m) - 1) * ldv;
+    for (int64_t j = lane; j < nv; j += 32) d[j] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// A warp sums one window's rows over 32 vectors of columns; warps past the windows zero
+// untouched table rows.
 template <bool F32, bool TF32>
 __global__ void __launch_bounds__(256) sum_kernel(const BwdArgs a, const uint32_t* key, const uint32_t* row) {
   pdl_wait();
@@ -263,7 +473,11 @@ __global__ void __launch_bounds__(256) sum_kernel(const BwdArgs a, const uint32_
   const int64_t nv = a.p.D / N, blocks = (nv + 31) / 32;
   const uint32_t none = uint32_t(a.p.Vt);
   const int64_t w = int64_t(blockIdx.x) * 8 + threadIdx.x / 32;
-  if (w >= a.plan.windows * blocks) return;
+  if (w >= a.plan.windows * blocks) {
+    const int64_t r0 = a.plan.fill + (w - a.plan.windows * blocks) * 32;
+    if (r0 < a.plan.fill_sum) zero_untouched<TF32>(a, key, r0, a.plan.fill_sum, lane);
+    return;
+  }
   const int64_t win = w / blocks, j = (w - win * blocks) * 32 + lane;
   const bool on = j < nv;
   const int64_t p0 = win * a.plan.window, p1 = min(p0 + a.plan.window, a.p.R);
@@ -319,42 +533,52 @@ __global__ void __launch_bounds__(256) sum_kernel(const BwdArgs a, const uint32_
 }
 
 // The segments that cross windows: the window a segment begins in adds the parts that the
-// windows after it left.
+// windows after it left.  Warps past the windows zero untouched table rows.
 template <bool F32, bool TF32>
 __global__ void __launch_bounds__(256) join_kernel(const BwdArgs a, const uint32_t* key) {
   pdl_wait();
   pdl_trigger();
-  constexpr int N = Vec<F32>::N;
+  constexpr int N = Vec<F32>::N, U = F32 ? 16 : 8;  // parts in flight
   const int lane = threadIdx.x & 31;
   const int64_t nv = a.p.D / N, blocks = (nv + 31) / 32;
   const int64_t w = int64_t(blockIdx.x) * 8 + threadIdx.x / 32;
-  if (w >= a.plan.windows * blocks) return;
+  if (w >= a.plan.windows * blocks) {
+    const int64_t r0 = a.plan.fill_sum + (w - a.plan.windows * blocks) * 32;
+    if (!a.accumulate && r0 < a.p.Vt) zero_untouched<TF32>(a, key, r0, a.p.Vt, lane);
+    return;
+  }
   const int64_t win = w / blocks, j = (w - win * blocks) * 32 + lane;
   const int64_t p0 = win * a.plan.window, p1 = p0 + a.plan.window;
   if (p1 >= a.p.R) return;
-  const uint32_t id = key[p1 - 1];
-  if (id == uint32_t(a.p.Vt) || key[p1] != id) return;                 // nothing goes on
-  if (p0 > 0 && key[p0 - 1] == id) return;                            // nor begins here
-  // the last window that begins with the id (the keys are sorted: bisection)
-  int64_t last = win + 1, past = a.plan.windows;
-  while (past - last > 1) {
-    const int64_t mid = (last + past) / 2;
-    if (key[mid * a.plan.window] == id) last = mid;
-    else past = mid;
+  const uint32_t id = key[p1 - 1], next = key[p1], prev = p0 > 0 ? key[p0 - 1] : ~0u;
+  if (id == uint32_t(a.p.Vt) || next != id || prev == id) return;  // nothing goes on, or nothing begins here
+  // the last window that begins with the id, 32 windows a look
+  int64_t last = win + 1;
+  for (;;) {
+    const int64_t x = last + 1 + lane;
+    const uint32_t m = __ballot_sync(0xffffffffu, x < a.plan.windows && key[x * a.plan.window] == id);
+    last += __popc(m);
+    if (m != 0xffffffffu) break;
   }
   if (j >= nv) return;
   float acc[N];
   const float* src = a.ws.part + (size_t(win) * 2 + 1) * a.p.D + j * N;
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = src[i];
-#pragma unroll 4
-  for (int64_t x = win + 1; x <= last; ++x) {
-    const float* q = a.ws.part + size_t(x) * 2 * a.p.D + j * N;
+  const int64_t stride = 2 * a.p.D;
+  for (int64_t x = win + 1; x <= last; x += U) {
+    const float* q = a.ws.part + size_t(x) * stride + j * N;
+    float4 f[U][N / 4];
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(q + i);
-      acc[i] += f.x, acc[i + 1] += f.y, acc[i + 2] += f.z, acc[i + 3] += f.w;
-    }
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i)
+        f[u][i] = x + u <= last ? *reinterpret_cast<const float4*>(q + u * stride + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i)
+        acc[4 * i] += f[u][i].x, acc[4 * i + 1] += f[u][i].y, acc[4 * i + 2] += f[u][i].z, acc[4 * i + 3] += f[u][i].w;
   }
   write_row<TF32, N>(a, id, j * N, acc);
 }
@@ -362,10 +586,12 @@ __global__ void __launch_bounds__(256) join_kernel(const BwdArgs a, const uint32
 template <bool F32, bool TF32>
 cudaError_t sums(const BwdArgs& a, const uint32_t* key, const uint32_t* row, cudaStream_t s) {
   const int64_t nv = a.p.D / Vec<F32>::N, warps = a.plan.windows * ((nv + 31) / 32);
-  PdlLaunch l((warps + 7) / 8, 256, 0, s);
+  const int64_t in_sum = (a.plan.fill_sum - a.plan.fill + 31) / 32;
+  const int64_t in_join = a.accumulate ? 0 : (a.p.Vt - a.plan.fill_sum + 31) / 32;
+  PdlLaunch l((warps + in_sum + 7) / 8, 256, 0, s);
   cudaError_t e = cudaLaunchKernelEx(&l.cfg, sum_kernel<F32, TF32>, a, key, row);
   if (e != cudaSuccess) return e;
-  PdlLaunch l2((warps + 7) / 8, 256, 0, s);
+  PdlLaunch l2((warps + in_join + 7) / 8, 256, 0, s);
   return cudaLaunchKernelEx(&l2.cfg, join_kernel<F32, TF32>, a, key);
 }
 
@@ -382,27 +608,26 @@ cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t s) {
 
 cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t s) {
   cudaError_t e;
-  const bool f32 = a.p.dtype == DSPARK_F32;
-  if (!a.accumulate) {
-    if (a.table_f32) zero_kernel<true><<<148 * 8, 256, 0, s>>>(a);
-    else zero_kernel<false><<<148 * 8, 256, 0, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
   int from = 0;
-  for (int k = 0; k < a.plan.passes; ++k) {
-    Pass ps{k * kDigitBits, k == 0, a.ws.key[from], a.ws.row[from], a.ws.key[1 - from], a.ws.row[1 - from]};
-    if (k == 0 && a.accumulate) {  // the first kernel of the call waits for all work before it
-      count_kernel<<<unsigned(a.plan.ctas + 1), kSortThreads, 0, s>>>(a, ps);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    } else {
-      PdlLaunch l(a.plan.ctas + (k == 0), kSortThreads, 0, s);
+  if (a.p.R <= kSmallRows) {
+    e = a.p.R <= kSmallRows / 4   ? small_sort<kSmallItems / 4>(a, s)
+        : a.p.R <= kSmallRows / 2 ? small_sort<kSmallItems / 2>(a, s)
+                                  : small_sort<kSmallItems>(a, s);
+    if (e != cudaSuccess) return e;
+  } else {
+    const int spare = a.plan.fill > 0 ? 148 * 3 : 0;
+    for (int k = 0; k < a.plan.passes; ++k) {
+      const Pass ps{k * kDigitBits, k, a.ws.key[from], a.ws.row[from], a.ws.key[1 - from], a.ws.row[1 - from]};
+      PdlLaunch l(a.plan.ctas + spare, kSortThreads, 0, s);
+      if (k == 0) l.cfg.numAttrs = 0;  // the first kernel of the call waits for all work before it
       if ((e = cudaLaunchKernelEx(&l.cfg, count_kernel, a, ps)) != cudaSuccess) return e;
+      PdlLaunch l2(a.plan.ctas + spare, kSortThreads, 0, s);
+      if ((e = cudaLaunchKernelEx(&l2.cfg, move_kernel, a, ps)) != cudaSuccess) return e;
+      from = 1 - from;
     }
-    PdlLaunch l(a.plan.ctas, kSortThreads, 0, s);
-    if ((e = cudaLaunchKernelEx(&l.cfg, move_kernel, a, ps)) != cudaSuccess) return e;
-    from = 1 - from;
   }
   const uint32_t *key = a.ws.key[from], *row = a.ws.row[from];
+  const bool f32 = a.p.dtype == DSPARK_F32;
   if (f32) return a.table_f32 ? sums<true, true>(a, key, row, s) : sums<true, false>(a, key, row, s);
   return a.table_f32 ? sums<false, true>(a, key, row, s) : sums<false, false>(a, key, row, s);
 }

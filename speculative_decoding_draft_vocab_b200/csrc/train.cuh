@@ -8,9 +8,13 @@ namespace dspark {
 namespace embed {
 
 constexpr int kSortThreads = 512;
-constexpr int kSortItems = 8;                          // per thread and chunk
+constexpr int kSortItems = 2;                          // per thread and chunk
 constexpr int kSortChunk = kSortThreads * kSortItems;  // rows ranked at a time
 constexpr int kSortCtas = 128;                         // at most: a CTA sorts a run of chunks
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallItems = 4;                         // rows per thread, at most
+constexpr int kSmallCtas = 8;
+constexpr int kSmallRows = kSmallThreads * kSmallItems * kSmallCtas;  // sorted by one cluster
 constexpr int kDigitBits = 9;
 constexpr int kDigits = 1 << kDigitBits;
 
@@ -27,6 +31,8 @@ struct Plan {
   int ctas;            // sorting CTAs
   int window;          // sorted rows per partial sum
   int64_t windows;
+  int64_t fill;        // table rows [0, fill) are zeroed beside the sort (0 when accumulating),
+  int64_t fill_sum;    // [fill, fill_sum) beside the windows' sums, the others beside the joins
 };
 
 inline Plan make_plan(int64_t R, int64_t Vt, int64_t D, bool f32) {
@@ -38,16 +44,27 @@ inline Plan make_plan(int64_t R, int64_t Vt, int64_t D, bool f32) {
   const int64_t chunks = (R + kSortChunk - 1) / kSortChunk;
   p.run = (chunks + kSortCtas - 1) / kSortCtas * kSortChunk;
   p.ctas = int((R + p.run - 1) / p.run);
-  // windows of 8 to 512 sorted rows: as long as about 32 warps per SM still have one each
+  // windows of 16 to 512 sorted rows: as long as 32 warps per SM still have one each
   const int64_t cols = f32 ? 128 : 256, blocks = (D + cols - 1) / cols;
-  p.window = 8;
+  p.window = 16;
   while (p.window < 512 && (R / (2 * p.window)) * blocks >= 148 * 32) p.window *= 2;
   p.windows = (R + p.window - 1) / p.window;
   return p;
 }
 
+// How the zeroing of the table's rows is spread over the kernels of the call: what fits the
+// time each spends waiting for latencies, the bulk beside the sums.
+inline void plan_fill(Plan& p, int64_t row_bytes) {
+  const double sort = p.R <= kSmallRows ? 64e6 : 24e6 * 2 * p.passes, join = 32e6;
+  const double total = double(p.Vt) * double(row_bytes);
+  const double f = total < sort + join ? total / (sort + join) : 1.0;
+  p.fill = int64_t(f * sort / double(row_bytes));
+  p.fill_sum = std::max(p.fill, p.Vt - int64_t(f * join / double(row_bytes)));
+}
+
 struct View {
   WsEmbedHeader* hdr;
+  uint32_t* flags;    // [ctas] error bits of the sorting CTAs' runs
   uint32_t* counts;   // [ctas][kDigits] digit counts of the sorting CTAs' runs
   uint32_t* key[2];   // [R] ids, sorted back and forth
   uint32_t* row[2];   // [R] the rows they came with
@@ -61,6 +78,7 @@ inline View view(void* base, const Plan& p) {
   uint8_t* b = static_cast<uint8_t*>(base);
   auto take = [&](size_t n) { uint8_t* at = b + off; off = align256(off + n); return at; };
   v.hdr = reinterpret_cast<WsEmbedHeader*>(take(sizeof(WsEmbedHeader)));
+  v.flags = reinterpret_cast<uint32_t*>(take(4 * size_t(p.ctas)));
   v.counts = reinterpret_cast<uint32_t*>(take(4 * size_t(p.ctas) * kDigits));
   for (int i = 0; i < 2; ++i) v.key[i] = reinterpret_cast<uint32_t*>(take(4 * size_t(p.R)));
   for (int i = 0; i < 2; ++i) v.row[i] = reinterpret_cast<uint32_t*>(take(4 * size_t(p.R)));
