@@ -49,9 +49,9 @@ __device__ __forceinline__ bool dropped(const dspark_embed_problem_t& p, int64_t
 __device__ __forceinline__ bool in_table(const dspark_embed_problem_t& p, int64_t id) { return id >= 0 && id < p.Vt; }
 
 // Whether any row that counts has an id outside the table; by one CTA, which also makes the
-// status word this call's.  Sixteen rows per thread in flight.
+// status word this call's.  Eight rows per thread in flight.
 __device__ void check_ids(const dspark_embed_problem_t& p, WsEmbedHeader* hdr) {
-  constexpr int U = 16;
+  constexpr int U = 8;
   int bad = 0;
   for (int64_t r0 = threadIdx.x; r0 < p.R; r0 += U * blockDim.x) {
     int64_t id[U];
@@ -70,11 +70,11 @@ __device__ void check_ids(const dspark_embed_problem_t& p, WsEmbedHeader* hdr) {
 }
 
 // ------------------------------------------------------------------ lookup
-// A warp takes one row's run of 4 x 32 16-byte vectors at a time; the last CTA checks the ids.
-constexpr int kFwdVecs = 4;
+// A warp takes one row's run of 2 x 32 16-byte vectors at a time; the last CTA checks the ids.
+constexpr int kFwdVecs = 2;
 
 template <bool F32>
-__global__ void __launch_bounds__(256) lookup_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(256, 8) lookup_kernel(const FwdArgs a) {
   if (blockIdx.x == gridDim.x - 1) {
     check_ids(a.p, a.hdr);
     return;
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(256) lookup_kernel(const FwdArgs a) {
         for (int i = 0; i < V::N; ++i) v[i] *= a.p.scale;
         o = V::put(v);
       }
-      dst[j0 + 32 * k] = o;
+      __stcs(dst + j0 + 32 * k, o);  // written once: the table's rows keep their place in L2
     }
   }
 }

@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const dspark_lce_pro
 // Work item w -> (m tile, n tile, K split).  Items run through groups of `group` m tiles,
 // m fastest inside a group: the tiles in flight at one time share both operands in L2.
 struct Work {
-  int m_tiles, n_tiles, ksplit, kchunks, group;
+  int m_tiles, n_tiles, kchunks, group;
   int bound_m, bound_k;  // the number of labelled rows bounds the tile rows / the K range
   const int32_t* n_valid;
 };
@@ -134,7 +134,7 @@ struct Item {
   int mt, nt, s, kc0, kc1;
 };
 
-__device__ __forceinline__ Item decode(const Work& wk, int w, int me, int kch) {
+__device__ __forceinline__ Item decode(const Work& wk, int w, int me, int kch, int ksplit) {
   Item it;
   const int per = me * wk.n_tiles;
   it.s = w / per;
@@ -146,8 +146,8 @@ __device__ __forceinline__ Item decode(const Work& wk, int w, int me, int kch) {
   const int gm = min(wk.group, me - m0);
   it.nt = t / gm;
   it.mt = m0 + (t - it.nt * gm);
-  it.kc0 = int((int64_t(it.s) * kch) / wk.ksplit);
-  it.kc1 = int((int64_t(it.s + 1) * kch) / wk.ksplit);
+  it.kc0 = int((int64_t(it.s) * kch) / ksplit);
+  it.kc1 = int((int64_t(it.s + 1) * kch) / ksplit);
   return it;
 }
 
@@ -155,7 +155,7 @@ enum : int { kFwd = 0, kDz = 1, kDh = 2, kDwBf16 = 3, kDwF32 = 4 };
 
 struct EpiArgs {
   View ws;
-  int64_t Rp;
+  Plan plan;
   int32_t rows, n_cols;      // rows and columns of the product that exist
   int32_t col0;              // first vocabulary id of the piece
   float z_alpha;
@@ -224,11 +224,6 @@ __device__ __forceinline__ void commit(uint32_t bar) {
   }
 }
 
-__device__ __forceinline__ void reduce_add_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
-  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%1, %2, %3}], [%4];"
-               ::"l"(map), "r"(x), "r"(y), "r"(z), "r"(src) : "memory");
-}
-
 __device__ __forceinline__ void st_shared_u4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -250,10 +245,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
 
 template <int CG>
 constexpr uint32_t stage_bytes() { return uint32_t(kBM * BK * 2 + 256 / CG * BK * 2); }
+// The bf16 dweight product has a short K range and much to write: its epilogue warps get two
+// staging tiles each, at the price of a stage.
+constexpr int staging_tiles(int epi) { return epi == kDwBf16 ? 2 : 1; }
 template <int CG>
-constexpr int stages() { return CG == 1 ? 4 : 6; }
+constexpr int stages(int epi) { return (CG == 1 ? 4 : 6) - (staging_tiles(epi) - 1); }
 template <int CG>
-constexpr size_t smem_bytes() { return size_t(stages<CG>()) * stage_bytes<CG>() + 1024 + kEpiWarps * 4096 + 1024; }
+constexpr size_t smem_bytes(int epi) {
+  return size_t(stages<CG>(epi)) * stage_bytes<CG>() + 1024 + size_t(staging_tiles(epi)) * kEpiWarps * 4096 + 1024;
+}
 
 // One epilogue warp's share of a tile: 32 rows (row = this thread's lane, `m0 + lane`) and the
 // columns [c0, c1) of the tile, at TMEM address `taddr` + column.  `n0`: first product
@@ -262,9 +262,11 @@ struct Share {
   uint32_t taddr;
   uint32_t sbuf;   // this warp's 4 KB staging tile
   int m0, n0, c0, c1;
-  int nt, half, split;
+  int nt, half;
+  int plane0;      // first row of the K split's plane
   bool empty;      // no K range: the product is zero and the accumulator was not written
   int n_valid, lane;
+  int boxes;       // boxes this warp has stored (picks one of two staging tiles)
 };
 
 // The staging tile may be written again once the TMA engine has read it.
@@ -322,7 +324,7 @@ __device__ __forceinline__ void fwd_finish(const EpiArgs& a, const Share& sh, co
     }
   }
   if (row < sh.n_valid)
-    a.ws.part[size_t(2 * sh.nt + sh.half) * a.Rp + row] = make_float2(mx, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+    a.ws.part[size_t(2 * sh.nt + sh.half) * a.plan.Rp + row] = make_float2(mx, (s4[0] + s4[1]) + (s4[2] + s4[3]));
 }
 
 // dL/dz = w g (p (1 + 2 z_alpha lse) - onehot), rounded once to bf16; zero past the last
@@ -383,20 +385,16 @@ __device__ __forceinline__ void f32_finish(const EpiArgs& a, const CUtensorMap& 
     staging_free(sh.lane);
     stage_row(sh.sbuf, sh.lane, o);
     if (sh.lane == 0) {
-      if constexpr (PLANES) {
-        if (a.add) reduce_add_3d(&out, sh.sbuf, sh.n0 + c, sh.m0, sh.split);
-        else tc::tma_store_3d(&out, sh.sbuf, sh.n0 + c, sh.m0, sh.split);
-      } else {
-        if (a.add) tc::tma_reduce_add_2d(&out, sh.sbuf, sh.n0 + c, sh.m0);
-        else tc::tma_store_2d(&out, sh.sbuf, sh.n0 + c, sh.m0);
-      }
+      const int y = PLANES ? sh.plane0 + sh.m0 : sh.m0;
+      if (a.add) tc::tma_reduce_add_2d(&out, sh.sbuf, sh.n0 + c, y);
+      else tc::tma_store_2d(&out, sh.sbuf, sh.n0 + c, y);
       tc::bulk_commit();
     }
   }
 }
 
 // dweight, rounded once to bf16
-__device__ __forceinline__ void bf16_finish(const EpiArgs& a, const CUtensorMap& out, const Share& sh) {
+__device__ __forceinline__ void bf16_finish(const EpiArgs& a, const CUtensorMap& out, Share& sh) {
   if (sh.m0 >= a.rows) return;
 #pragma unroll 1
   for (int c = sh.c0; c < sh.c1 && sh.n0 + c < a.n_cols; c += 64) {
@@ -409,10 +407,12 @@ __device__ __forceinline__ void bf16_finish(const EpiArgs& a, const CUtensorMap&
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[16 * h + i] = sh.empty ? 0u : pack_bf16(v[2 * i], v[2 * i + 1]);
     }
-    staging_free(sh.lane);
-    stage_row(sh.sbuf, sh.lane, o);
+    const uint32_t buf = sh.sbuf + uint32_t(sh.boxes++ & 1) * 4096u;
+    if (sh.lane == 0) tc::bulk_wait_read<1>();  // the store before the last has read this tile
+    __syncwarp();
+    stage_row(buf, sh.lane, o);
     if (sh.lane == 0) {
-      tc::tma_store_2d(&out, sh.sbuf, sh.n0 + c, sh.m0);
+      tc::tma_store_2d(&out, buf, sh.n0 + c, sh.m0);
       tc::bulk_commit();
     }
   }
@@ -426,7 +426,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                const __grid_constant__ CUtensorMap tmO, const Work wk, const EpiArgs ea, const int bn) {
   constexpr bool A_MN = EPI == kDwBf16 || EPI == kDwF32;
   constexpr bool B_MN = EPI != kFwd && EPI != kDz;
-  constexpr int STAGES = stages<CG>();
+  constexpr int STAGES = stages<CG>(EPI);
   // The tensor cores' FP32 accumulation rounds towards zero: over K = 4096 the logits come
   // out 2.2e-6 short (relative), over K = 512 3e-7.  The forward hands over its accumulator
   // every 512 values of K and the epilogue adds the segments in registers, rounding to
@@ -478,7 +478,8 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const int n_valid = *wk.n_valid;
   const int me = wk.bound_m ? min(wk.m_tiles, (n_valid + kBM * CG - 1) / (kBM * CG)) : wk.m_tiles;
   const int kch = wk.bound_k ? min(wk.kchunks, (n_valid + BK - 1) / BK) : wk.kchunks;
-  const int W = me * wk.n_tiles * wk.ksplit;  // the same in every role
+  const int ks = EPI == kDh ? splits_of(ea.plan, me) : 1;
+  const int W = me * wk.n_tiles * ks;  // the same in every role
   bool timed_out = false;
 
   if (warp == 0 && lane == 0) {
@@ -487,7 +488,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const uint32_t tx = CG * (SA + uint32_t(bnc) * BK * 2);
     int it = 0;
     for (int w = tile0; w < W; w += tiles_step) {
-      const Item t = decode(wk, w, me, kch);
+      const Item t = decode(wk, w, me, kch, ks);
       const int am = (t.mt * CG + int(rank)) * kBM, bn0 = t.nt * bn + int(rank) * bnc;
       for (int kc = t.kc0; kc < t.kc1; ++kc, ++it) {
         const int st = it % STAGES;
@@ -516,7 +517,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const uint32_t idesc = tc::idesc_bf16(kBM * CG, bn, A_MN, B_MN);
     int it = 0, tl = 0;
     for (int w = tile0; w < W; w += tiles_step) {
-      const Item t = decode(wk, w, me, kch);
+      const Item t = decode(wk, w, me, kch, ks);
       int kc = t.kc0;
       do {  // one accumulator per segment (an empty K range still hands one over)
         const int b = tl & 1;
@@ -547,9 +548,12 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lanes = uint32_t(q * 32) << 16;
     Share sh;
-    sh.sbuf = smem_u32(stage + (warp - 2) * 4096);
+    sh.sbuf = smem_u32(stage + (warp - 2) * staging_tiles(EPI) * 4096);
+    sh.boxes = 0;
     sh.half = half, sh.n_valid = n_valid, sh.lane = lane;
-    sh.c0 = half * (bn / 2), sh.c1 = sh.c0 + bn / 2;
+    // the forward's halves are even; the others' are whole 64-column boxes
+    const int first = EPI == kFwd ? bn / 2 : (bn / 64 + 1) / 2 * 64;
+    sh.c0 = half ? first : 0, sh.c1 = half ? bn : first;
     auto release = [&](int b) {
       tc::fence_before_sync();
       __syncwarp();
@@ -561,9 +565,9 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     };
     int tl = 0;
     for (int w = tile0; w < W; w += tiles_step) {
-      const Item t = decode(wk, w, me, kch);
+      const Item t = decode(wk, w, me, kch, ks);
       sh.m0 = (t.mt * CG + int(rank)) * kBM + q * 32, sh.n0 = t.nt * bn;
-      sh.nt = t.nt, sh.split = t.s, sh.empty = t.kc0 == t.kc1;
+      sh.nt = t.nt, sh.plane0 = t.s * me * kBM * CG, sh.empty = t.kc0 == t.kc1;
       if constexpr (EPI == kFwd) {
         float z[128];
 #pragma unroll
@@ -687,6 +691,8 @@ __global__ void __launch_bounds__(256) dhidden_kernel(const View ws, const Plan 
   pdl_wait();
   pdl_trigger();
   const int64_t h8 = pl.H / 8, n = pl.R * h8;
+  const int tile = kBM * pl.cg, me = (ws.hdr->n_valid + tile - 1) / tile, splits = splits_of(pl, me);
+  const size_t plane = size_t(me) * tile * pl.H;
   for (int64_t k = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; k < n; k += int64_t(gridDim.x) * blockDim.x) {
     const int64_t r = k / h8, j = (k - r * h8) * 8;
     const int i = ws.index[r];
@@ -694,8 +700,8 @@ __global__ void __launch_bounds__(256) dhidden_kernel(const View ws, const Plan 
     if (i >= 0) {
       float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       const float* src = ws.planes + size_t(i) * pl.H + j;
-#pragma unroll 2
-      for (int s = 0; s < pl.ksplit; ++s, src += size_t(pl.R) * pl.H) {
+#pragma unroll 4
+      for (int s = 0; s < splits; ++s, src += plane) {
         const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 4);
         a[0] += x.x, a[1] += x.y, a[2] += x.z, a[3] += x.w;
         a[4] += y.x, a[5] += y.y, a[6] += y.z, a[7] += y.w;
@@ -716,11 +722,12 @@ template <int CG, int EPI>
 cudaError_t product_cg(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const Work& wk,
                        const EpiArgs& ea, int bn, cudaStream_t s) {
   auto kern = product_kernel<CG, EPI>;
-  constexpr size_t smem = smem_bytes<CG>();
+  constexpr size_t smem = smem_bytes<CG>(EPI);
   // per device, so set on every call (it is a host-side table entry)
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  const int64_t W = int64_t(wk.m_tiles) * wk.n_tiles * wk.ksplit;
+  // K splits (hidden gradient) make more items of few tiles
+  const int64_t W = int64_t(wk.m_tiles) * wk.n_tiles * (EPI == kDh ? kMaxSplit : 1);
   const int64_t grid = std::min<int64_t>(W, std::max(1, tc::sm_count() / CG)) * CG;
   PdlLaunch l(grid, kThreads, smem, s, CG);
   return cudaLaunchKernelEx(&l.cfg, kern, a, b, o, wk, ea, bn);
@@ -747,10 +754,10 @@ cudaError_t launch_fwd(const dspark_lce_problem_t& p, const dspark_lce_out_t& ou
   if (!tc::make_map(&ma, ws.hsup, pl.Rp, p.H, p.H, 64, kBM) ||
       !tc::make_map(&mb, p.weight, p.V, p.H, p.weight_ld, 64, pl.bn_fwd / pl.cg))
     return cudaErrorInvalidValue;
-  Work wk{tiles(p.R, kBM * pl.cg), tiles(p.V, pl.bn_fwd), 1, tiles(p.H, BK), 16, 1, 0, &ws.hdr->n_valid};
+  Work wk{tiles(p.R, kBM * pl.cg), tiles(p.V, pl.bn_fwd), tiles(p.H, BK), 16, 1, 0, &ws.hdr->n_valid};
   EpiArgs ea{};
   ea.ws = ws;
-  ea.Rp = pl.Rp;
+  ea.plan = pl;
   ea.rows = int32_t(pl.Rp);
   ea.n_cols = int32_t(p.V);
   if ((e = product<kFwd>(pl, ma, mb, ma, wk, ea, pl.bn_fwd, s)) != cudaSuccess) return e;
@@ -775,21 +782,21 @@ cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& 
       return cudaErrorInvalidValue;
     EpiArgs ea{};
     ea.ws = ws;
-    ea.Rp = pl.Rp;
+    ea.plan = pl;
     ea.rows = int32_t(pl.Rp);
     ea.n_cols = int32_t(n);
     ea.col0 = int32_t(v0);
     ea.z_alpha = p.z_alpha;
     ea.grad_scale = g.grad_scale;
-    const Work wz{tiles(p.R, kBM * pl.cg), tiles(n, pl.bn_dz), 1, tiles(p.H, BK), 16, 1, 0, &ws.hdr->n_valid};
+    const Work wz{tiles(p.R, kBM * pl.cg), tiles(n, pl.bn_dz), tiles(p.H, BK), 16, 1, 0, &ws.hdr->n_valid};
     if ((e = product<kDz>(pl, h_k, w_k, z_out, wz, ea, pl.bn_dz, s)) != cudaSuccess) return e;
     if (g.dhidden) {
       if (!tc::make_map(&w_mn, w0, n, p.H, p.weight_ld, 64, 64) || !tc::make_map(&z_k, ws.dz, pl.Rp, ldz, ldz, 64, kBM) ||
-          !tc::make_out_map(&o, ws.planes, pl.R, p.H, p.H, pl.ksplit, size_t(pl.R) * p.H))
+          !tc::make_out_map(&o, ws.planes, pl.plane_rows, p.H, p.H))
         return cudaErrorInvalidValue;
       ea.n_cols = int32_t(p.H);
       ea.add = i > 0;
-      const Work wh{tiles(p.R, kBM * pl.cg), tiles(p.H, pl.bn_h), pl.ksplit, tiles(n, BK), 8, 1, 0, &ws.hdr->n_valid};
+      const Work wh{tiles(p.R, kBM * pl.cg), tiles(p.H, pl.bn_h), tiles(n, BK), 8, 1, 0, &ws.hdr->n_valid};
       if ((e = product<kDh>(pl, z_k, w_mn, o, wh, ea, pl.bn_h, s)) != cudaSuccess) return e;
     }
     if (g.dweight) {
@@ -800,7 +807,7 @@ cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& 
       ea.rows = int32_t(n);
       ea.n_cols = int32_t(p.H);
       ea.add = g.accumulate ? 1 : 0;
-      const Work ww{tiles(n, kBM * pl.cg), tiles(p.H, pl.bn_h), 1, tiles(p.R, BK), 8, 0, 1, &ws.hdr->n_valid};
+      const Work ww{tiles(n, kBM * pl.cg), tiles(p.H, pl.bn_h), tiles(p.R, BK), 1, 0, 1, &ws.hdr->n_valid};
       e = f32 ? product<kDwF32>(pl, z_mn, h_mn, o, ww, ea, pl.bn_h, s)
               : product<kDwBf16>(pl, z_mn, h_mn, o, ww, ea, pl.bn_h, s);
       if (e != cudaSuccess) return e;

@@ -9,6 +9,9 @@ namespace lce {
 constexpr int kBM = 128;                             // tile rows per CTA (TMEM lanes)
 constexpr int kSlots = 148;                          // SMs the plan assumes
 constexpr size_t kPieceBytes = size_t(256) << 20;    // bound on the kept piece of dz
+constexpr int kMaxSplitTiles = 32;                   // more row tiles than this are not split
+constexpr int kMaxSplit = 32;
+constexpr size_t kPlaneBytes = size_t(96) << 20;     // bound on split planes (they stay in L2)
 constexpr int kMergeRows = 32;                       // rows per CTA of the merge kernel
 
 struct WsLceHeader {
@@ -30,7 +33,8 @@ struct Plan {
   int64_t fwd_tiles;   // vocabulary tiles of the forward product
   int64_t piece;       // vocabulary columns per piece of the backward
   int pieces;
-  int ksplit;          // K splits of the hidden gradient (planes of partial sums)
+  int64_t plane_rows;  // rows of the hidden gradient's partial sums, all planes together
+  uint8_t ksplit[kMaxSplitTiles + 1];  // its K splits (planes) by the number of row tiles
   int64_t merge_blocks;
 };
 
@@ -46,29 +50,61 @@ struct View {
   uint16_t* hsup;      // [Rp][H] bf16 labelled hidden rows, compact, zeros up to a whole chunk
   float2* part;        // [2 fwd_tiles][Rp] (base-2 maximum, sum) of a row's columns in half a tile
   uint16_t* dz;        // [Rp][piece] bf16 piece of dL/dlogits
-  float* planes;       // [ksplit][R][H] partial sums of the hidden gradient
+  float* planes;       // [splits][row tiles' rows][H] partial sums of the hidden gradient
 };
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Columns per tile for `m` row tiles over n columns: the widest tile has the fewest operand
+// bytes per product, but the last wave of tiles over the SMs should be full.  `per` is the
+// step of widths the product can take.
+inline int pick_columns(int64_t m, int64_t n, int64_t slots, int per) {
+  int best = 256;
+  int64_t cost = INT64_MAX;
+  for (int bn = 256; bn >= 128; bn -= per) {
+    const int64_t c = ceil_div(m * ceil_div(n, bn), slots) * (bn + 8);  // 8: a tile's fixed part
+    if (c < cost) cost = c, best = bn;
+  }
+  return best;
+}
 
 inline Plan make_plan(int64_t R, int64_t V, int64_t H) {
   Plan p{};
   p.R = R, p.V = V, p.H = H;
   p.Rp = ceil_div(R, 64) * 64;
   p.cg = R > kBM ? 2 : 1;
-  p.bn_fwd = p.bn_dz = 256;
+  const int64_t slots = kSlots / p.cg, m_tiles = ceil_div(R, kBM * p.cg);
+  p.bn_fwd = pick_columns(m_tiles, V, slots, 16);
   p.bn_h = H > 128 ? 256 : 128;
   p.fwd_tiles = ceil_div(V, p.bn_fwd);
   const int64_t most = std::max<int64_t>(256, int64_t(kPieceBytes / (2 * size_t(p.Rp))) / 256 * 256);
   p.pieces = int(ceil_div(V, most));
   p.piece = ceil_div(ceil_div(V, p.pieces), 256) * 256;
   p.pieces = int(ceil_div(V, p.piece));
-  // few row and hidden tiles: the K range (the piece's vocabulary) is split so that every
-  // SM has work, each split at least eight 64-wide chunks long
-  const int64_t tiles = ceil_div(R, kBM * p.cg) * ceil_div(H, p.bn_h);
-  p.ksplit = int(std::max<int64_t>(1, std::min<int64_t>(kSlots / p.cg / tiles, p.piece / 512)));
+  p.bn_dz = pick_columns(m_tiles, std::min(V, p.piece), slots, 64);
+  // Few row and hidden tiles: the K range (the piece's vocabulary) is split so that the waves
+  // of tiles over the SMs are full.  How many row tiles there are only the device knows (they
+  // hold the labelled rows), so there is a number of splits for each count.
+  const int64_t n_tiles = ceil_div(H, p.bn_h), chunks = ceil_div(std::min(V, p.piece), 64);
+  p.plane_rows = R;
+  for (int64_t m = 1; m <= kMaxSplitTiles; ++m) {
+    int best = 1;
+    int64_t cost = INT64_MAX;
+    for (int k = 1; k <= kMaxSplit && (k == 1 || chunks / k >= 8); ++k) {
+      if (k > 1 && size_t(m * k * kBM * p.cg) * size_t(H) * 4 > kPlaneBytes) break;
+      const int64_t c = ceil_div(m * n_tiles * k, slots) * (ceil_div(chunks, k) + 12);  // 12: writing the sums
+      if (c < cost) cost = c, best = k;
+    }
+    p.ksplit[m] = uint8_t(best);
+    if (m <= m_tiles && best > 1) p.plane_rows = std::max(p.plane_rows, m * best * kBM * p.cg);
+  }
   p.merge_blocks = ceil_div(R, kMergeRows);
   return p;
+}
+
+// K splits and rows per plane of the hidden gradient for n labelled rows.
+__host__ __device__ inline int splits_of(const Plan& p, int row_tiles) {
+  return row_tiles >= 1 && row_tiles <= kMaxSplitTiles ? p.ksplit[row_tiles] : 1;
 }
 
 struct Offsets {
@@ -92,7 +128,7 @@ inline Offsets offsets(const Plan& p, bool bwd, bool dhidden) {
   take(o.part, sizeof(float2) * 2 * size_t(p.fwd_tiles) * Rp);
   o.fwd_bytes = off;
   take(o.dz, bwd ? 2 * Rp * size_t(p.piece) : 0);
-  take(o.planes, bwd && dhidden ? sizeof(float) * size_t(p.ksplit) * R * size_t(p.H) : 0);
+  take(o.planes, bwd && dhidden ? sizeof(float) * size_t(p.plane_rows) * size_t(p.H) : 0);
   o.bytes = off;
   return o;
 }
