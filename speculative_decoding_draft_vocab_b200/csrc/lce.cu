@@ -17,6 +17,7 @@
 //   warp 0      one thread issues the TMA loads into a ring of 64-wide K stages
 //   warp 1      allocates TMEM; one thread (of the tile's first CTA) issues the MMAs
 //   warps 2..9  read the accumulator (a thread: one tile row, half the columns), finish it
+//   warp 10     (pair) passes on that both CTAs are done with an accumulator
 // The accumulator is double-buffered in TMEM: a tile's epilogue runs beside the next
 // tile's MMAs.
 #include <cuda_bf16.h>
@@ -33,12 +34,13 @@ namespace {
 
 using tc::BK;
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kRelayWarp = 2 + kEpiWarps;
+constexpr int kThreads = 32 * (kRelayWarp + 1);
 
 // ------------------------------------------------------------------ prep
 // Each CTA takes a contiguous run of rows, counts the labelled rows before it (the labels
-// are small and in L2) and writes its part of the list; then its warps copy the labelled
-// hidden rows.  The last CTA, which sees every row, writes the counts and the status and
+// are small and in L2) and writes its part of the list; then it copies its labelled hidden
+// rows.  The last CTA, which sees every row, writes the counts and the status and
 // zero-fills the compact rows up to a whole 64-row K chunk: the dweight product reads
 // those, and zero is what they have to add.
 constexpr int kPrepThreads = 256;
@@ -47,7 +49,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const dspark_lce_pro
                                                             int64_t* num_tokens, int64_t rows_per_cta) {
   pdl_trigger();
   __shared__ int sh_warp[kPrepThreads / 32];
-  __shared__ int sh_before, sh_bad, sh_pos[kPrepThreads];
+  __shared__ int sh_before, sh_bad, sh_row[kPrepThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t r0 = int64_t(blockIdx.x) * rows_per_cta;
   const int64_t r1 = r0 + rows_per_cta < p.R ? r0 + rows_per_cta : p.R;
@@ -56,12 +58,18 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const dspark_lce_pro
   __syncthreads();
   // labelled rows before r0 (and, in the last CTA, any label out of range)
   int n = 0, bad = 0;
-  for (int64_t r = tid; r < (last ? r1 : r0); r += kPrepThreads) {
-    const int64_t t = p.targets[r];
-    const bool in = t >= 0 && t < p.V;
-    if (t != p.ignore_index) {
-      if (!in) bad = 1;
-      else if (r < r0) ++n;
+  const int64_t seen = last ? r1 : r0;
+  for (int64_t r8 = tid; r8 < seen; r8 += 8 * kPrepThreads) {
+    int64_t t[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) t[u] = r8 + u * kPrepThreads < seen ? p.targets[r8 + u * kPrepThreads] : p.ignore_index;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const bool in = t[u] >= 0 && t[u] < p.V;
+      if (t[u] != p.ignore_index) {
+        if (!in) bad = 1;
+        else if (r8 + u * kPrepThreads < r0) ++n;
+      }
     }
   }
   n = __reduce_add_sync(0xffffffffu, n);
@@ -92,17 +100,28 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const dspark_lce_pro
       ws.tok[at] = int32_t(t);
       ws.w[at] = p.row_weight ? p.row_weight[r] : 1.f;
     }
-    sh_pos[tid] = live ? at : -1;
+    if (live) sh_row[at - base] = tid;
     __syncthreads();
-    // the labelled rows of this run: one warp per row
-    for (int k = warp; k < kPrepThreads && c0 + k < r1; k += kPrepThreads / 32) {
-      const int pos = sh_pos[k];
-      if (pos < 0) continue;  // the whole warp
-      const uint4* src =
-          reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.hidden) + size_t(c0 + k) * p.hidden_ld);
-      uint4* dst = reinterpret_cast<uint4*>(ws.hsup + size_t(pos) * p.H);
-#pragma unroll 4
-      for (int64_t j = lane; j < p.H / 8; j += 32) dst[j] = src[j];
+    // this run's labelled rows, four 16-byte vectors per thread in flight
+    const int h8 = int(p.H / 8);
+    const int64_t n_vec = int64_t(total) * h8;
+    uint4* dst = reinterpret_cast<uint4*>(ws.hsup + size_t(base) * p.H);
+    for (int64_t j0 = tid; j0 < n_vec; j0 += 4 * kPrepThreads) {
+      uint4 q[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t j = j0 + u * kPrepThreads;
+        if (j >= n_vec) break;
+        const int k = int(j / h8), v = int(j - int64_t(k) * h8);
+        q[u] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.hidden) +
+                                              size_t(c0 + sh_row[k]) * p.hidden_ld)[v];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t j = j0 + u * kPrepThreads;
+        if (j >= n_vec) break;
+        dst[j] = q[u];
+      }
     }
     __syncthreads();
     base += total;
@@ -163,29 +182,12 @@ struct EpiArgs {
   int32_t add;               // dh: add to the planes; dw: add to dweight
 };
 
-template <int CG>
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
-  if constexpr (CG == 1) {
-    return mbar_wait_bounded(bar, parity);
-  } else {
-    // arrivals may come from the other CTA of the pair: acquire at cluster scope
-    auto test = [&]() {
-      uint32_t done;
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(done) : "r"(bar), "r"(parity) : "memory");
-      return done != 0;
-    };
-    if (test()) return true;
-    const uint64_t t0 = global_timer_ns();
-    for (;;) {
-      for (int i = 0; i < 64; ++i)
-        if (test()) return true;
-      if (global_timer_ns() - t0 > kWaitLimitNs) return false;
-    }
-  }
+// Acquire at cluster scope of a barrier phase already seen complete.
+__device__ __forceinline__ void acquire_cluster(uint32_t bar, uint32_t parity) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}"
+      ::"r"(bar), "r"(parity) : "memory");
 }
 
 // TMA tile load completing on the barrier of the tile's first CTA.
@@ -228,19 +230,29 @@ __device__ __forceinline__ void st_shared_u4(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// 16 consecutive fp32 columns of this thread's TMEM lane (warp-collective).
+// 16 or 32 consecutive fp32 columns of this thread's TMEM lane (warp-collective).  The values
+// are there after tmem_wait, which names them, so that no use of them moves before it.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
-  __syncwarp();
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
       "%15}, [%16];"
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
         "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
       : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait16(float* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
                  "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
                  "+f"(v[15])::"memory");
+}
+// This warp's share of an accumulator, 128 columns: all loads in flight, then one wait.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) tmem_ld16(taddr + uint32_t(16 * i), v + 16 * i);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) tmem_wait16(v + 16 * i);
 }
 
 template <int CG>
@@ -255,13 +267,11 @@ constexpr size_t smem_bytes(int epi) {
   return size_t(stages<CG>(epi)) * stage_bytes<CG>() + 1024 + size_t(staging_tiles(epi)) * kEpiWarps * 4096 + 1024;
 }
 
-// One epilogue warp's share of a tile: 32 rows (row = this thread's lane, `m0 + lane`) and the
-// columns [c0, c1) of the tile, at TMEM address `taddr` + column.  `n0`: first product
-// column of the tile.
+// One epilogue warp's share of a tile: 32 rows (row = this thread's lane, `m0 + lane`) and
+// `cols` columns of the tile from c0 on.  `n0`: first product column of the tile.
 struct Share {
-  uint32_t taddr;
-  uint32_t sbuf;   // this warp's 4 KB staging tile
-  int m0, n0, c0, c1;
+  uint32_t sbuf;   // this warp's 4 KB staging tile (or two of them)
+  int m0, n0, c0, cols;
   int nt, half;
   int plane0;      // first row of the K split's plane
   bool empty;      // no K range: the product is zero and the accumulator was not written
@@ -269,28 +279,12 @@ struct Share {
   int boxes;       // boxes this warp has stored (picks one of two staging tiles)
 };
 
-// The staging tile may be written again once the TMA engine has read it.
-__device__ __forceinline__ void staging_free(int lane) {
-  if (lane == 0) tc::bulk_wait_read<0>();
-  __syncwarp();
-}
-
-// 32 rows x 128 bytes, 16-byte chunk k of row `lane` at chunk k ^ (lane % 8): the 128-byte swizzle
-__device__ __forceinline__ void stage_row(uint32_t sbuf, int lane, const uint32_t* o) {
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    st_shared_u4(sbuf + uint32_t(lane) * 128u + uint32_t((k ^ (lane & 7)) * 16), o[4 * k], o[4 * k + 1], o[4 * k + 2],
-                 o[4 * k + 3]);
-  tc::fence_proxy_async_smem();
-  __syncwarp();
-}
-
 // Forward: (maximum, sum) of the row's exponentials over this share, base 2, and the logit
 // at the label, from the row's logits in registers.
 __device__ __forceinline__ void fwd_finish(const EpiArgs& a, const Share& sh, const float (&z)[128]) {
   const int row = sh.m0 + sh.lane;
   const int tgt = row < sh.n_valid ? a.ws.tok[row] - sh.n0 - sh.c0 : -1;
-  const int cols = min(sh.c1, a.n_cols - sh.n0) - sh.c0;  // <= 0: wholly past the vocabulary
+  const int cols = min(sh.cols, a.n_cols - sh.n0 - sh.c0);  // <= 0: wholly past the vocabulary
   float zt = 0.f;
   float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -327,26 +321,48 @@ __device__ __forceinline__ void fwd_finish(const EpiArgs& a, const Share& sh, co
     a.ws.part[size_t(2 * sh.nt + sh.half) * a.plan.Rp + row] = make_float2(mx, (s4[0] + s4[1]) + (s4[2] + s4[3]));
 }
 
+// 32 rows x 64 bf16 columns of the share, from packed words, to the output at (x, y)
+__device__ __forceinline__ void store_box(Share& sh, const CUtensorMap& out, const uint32_t* o, int x, int y, int mode,
+                                          int tiles) {
+  const uint32_t buf = sh.sbuf + (tiles == 2 ? uint32_t(sh.boxes++ & 1) * 4096u : 0u);
+  if (sh.lane == 0) {  // the store that last used this staging tile has read it
+    if (tiles == 2) tc::bulk_wait_read<1>();
+    else tc::bulk_wait_read<0>();
+  }
+  __syncwarp();
+  // 16-byte chunk k of row `lane` at chunk k ^ (lane % 8): the 128-byte swizzle
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    st_shared_u4(buf + uint32_t(sh.lane) * 128u + uint32_t((k ^ (sh.lane & 7)) * 16), o[4 * k], o[4 * k + 1],
+                 o[4 * k + 2], o[4 * k + 3]);
+  tc::fence_proxy_async_smem();
+  __syncwarp();
+  if (sh.lane == 0) {
+    if (mode) tc::tma_reduce_add_2d(&out, buf, x, y);
+    else tc::tma_store_2d(&out, buf, x, y);
+    tc::bulk_commit();
+  }
+}
+
 // dL/dz = w g (p (1 + 2 z_alpha lse) - onehot), rounded once to bf16; zero past the last
 // labelled row and past the vocabulary (those enter the gradient products).
-__device__ __forceinline__ void dz_finish(const EpiArgs& a, const CUtensorMap& out, const Share& sh) {
+__device__ __forceinline__ void dz_finish(const EpiArgs& a, const CUtensorMap& out, Share& sh, float (&z)[128]) {
   if (sh.m0 >= a.rows) return;  // the whole warp
   const int row = sh.m0 + sh.lane;
   const bool live = row < sh.n_valid;
-  const int tgt = live ? a.ws.tok[row] - a.col0 - sh.n0 : -1;
+  const int n0 = sh.n0 + sh.c0;
+  const int tgt = live ? a.ws.tok[row] - a.col0 - n0 : -1;
   const float lse2 = live ? a.ws.lse2[row] : 0.f;
   const float gw = live ? a.ws.w[row] * (a.grad_scale ? *a.grad_scale : 1.f) : 0.f;
   const float scale = gw * fmaf(2.f * a.z_alpha, lse2 * kLn2, 1.f);
-  const int cols = live ? a.n_cols - sh.n0 : 0;
-#pragma unroll 1
-  for (int c = sh.c0; c < sh.c1; c += 64) {
+  const int cols = live ? a.n_cols - n0 : 0;
+#pragma unroll
+  for (int c = 0; c < 128; c += 64) {
     uint32_t o[32];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float v[32];
-      __syncwarp();  // the TMEM load is warp-collective
-      tc::tmem_ld32(sh.taddr + uint32_t(c + 32 * h), v);
       const int cc = c + 32 * h;
+      float* v = z + cc;
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = ex2(fmaf(v[i], kLog2e, -lse2)) * scale;
       if (uint32_t(tgt - cc) < 32u) {
@@ -360,61 +376,35 @@ __device__ __forceinline__ void dz_finish(const EpiArgs& a, const CUtensorMap& o
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[16 * h + i] = pack_bf16(v[2 * i], v[2 * i + 1]);
     }
-    staging_free(sh.lane);
-    stage_row(sh.sbuf, sh.lane, o);
-    if (sh.lane == 0) {
-      tc::tma_store_2d(&out, sh.sbuf, sh.n0 + c, sh.m0);
-      tc::bulk_commit();
-    }
+    store_box(sh, out, o, n0 + c, sh.m0, 0, staging_tiles(kDz));
   }
 }
 
 // FP32 results: dhidden's partial sums (one plane per K split; a plane's element gets one
 // addition per piece, in stream order, so the sums have a fixed order), or dweight.
-template <bool PLANES>
-__device__ __forceinline__ void f32_finish(const EpiArgs& a, const CUtensorMap& out, const Share& sh) {
-  if (sh.m0 >= (PLANES ? sh.n_valid : a.rows) || (sh.empty && a.add)) return;
-#pragma unroll 1
-  for (int c = sh.c0; c < sh.c1 && sh.n0 + c < a.n_cols; c += 32) {
-    float v[32];
-    uint32_t o[32];
-    __syncwarp();
-    tc::tmem_ld32(sh.taddr + uint32_t(c), v);
+template <int EPI>
+__device__ __forceinline__ void f32_finish(const EpiArgs& a, const CUtensorMap& out, Share& sh, const float (&z)[128]) {
+  if (sh.m0 >= (EPI == kDh ? sh.n_valid : a.rows) || (sh.empty && a.add)) return;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = sh.empty ? 0u : __float_as_uint(v[i]);
-    staging_free(sh.lane);
-    stage_row(sh.sbuf, sh.lane, o);
-    if (sh.lane == 0) {
-      const int y = PLANES ? sh.plane0 + sh.m0 : sh.m0;
-      if (a.add) tc::tma_reduce_add_2d(&out, sh.sbuf, sh.n0 + c, y);
-      else tc::tma_store_2d(&out, sh.sbuf, sh.n0 + c, y);
-      tc::bulk_commit();
-    }
+  for (int c = 0; c < 128; c += 32) {
+    if (c >= sh.cols || sh.n0 + sh.c0 + c >= a.n_cols) break;
+    uint32_t o[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = sh.empty ? 0u : __float_as_uint(z[c + i]);
+    store_box(sh, out, o, sh.n0 + sh.c0 + c, (EPI == kDh ? sh.plane0 : 0) + sh.m0, a.add, staging_tiles(EPI));
   }
 }
 
 // dweight, rounded once to bf16
-__device__ __forceinline__ void bf16_finish(const EpiArgs& a, const CUtensorMap& out, Share& sh) {
+__device__ __forceinline__ void bf16_finish(const EpiArgs& a, const CUtensorMap& out, Share& sh, const float (&z)[128]) {
   if (sh.m0 >= a.rows) return;
-#pragma unroll 1
-  for (int c = sh.c0; c < sh.c1 && sh.n0 + c < a.n_cols; c += 64) {
+#pragma unroll
+  for (int c = 0; c < 128; c += 64) {
+    if (c >= sh.cols || sh.n0 + sh.c0 + c >= a.n_cols) break;
     uint32_t o[32];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[32];
-      __syncwarp();
-      tc::tmem_ld32(sh.taddr + uint32_t(c + 32 * h), v);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[16 * h + i] = sh.empty ? 0u : pack_bf16(v[2 * i], v[2 * i + 1]);
-    }
-    const uint32_t buf = sh.sbuf + uint32_t(sh.boxes++ & 1) * 4096u;
-    if (sh.lane == 0) tc::bulk_wait_read<1>();  // the store before the last has read this tile
-    __syncwarp();
-    stage_row(buf, sh.lane, o);
-    if (sh.lane == 0) {
-      tc::tma_store_2d(&out, buf, sh.n0 + c, sh.m0);
-      tc::bulk_commit();
-    }
+    for (int i = 0; i < 32; ++i) o[i] = sh.empty ? 0u : pack_bf16(z[c + 2 * i], z[c + 2 * i + 1]);
+    store_box(sh, out, o, sh.n0 + sh.c0 + c, sh.m0, 0, staging_tiles(kDwBf16));
   }
 }
 
@@ -431,7 +421,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   // out 2.2e-6 short (relative), over K = 512 3e-7.  The forward hands over its accumulator
   // every 512 values of K and the epilogue adds the segments in registers, rounding to
   // nearest; the other products are rounded to bf16 right after, where it does not show.
-  constexpr int SEG = EPI == kFwd ? 512 / BK : 1 << 30;
+  constexpr int SEG = EPI == kFwd ? 512 / BK : 1 << 29;
   constexpr uint32_t SA = kBM * BK * 2, SS = stage_bytes<CG>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -440,7 +430,10 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const uint32_t empty0 = full0 + 8 * STAGES;
   const uint32_t accf0 = empty0 + 8 * STAGES;
   const uint32_t acce0 = accf0 + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 4);
+  // what the MMA thread waits on for an accumulator: with one CTA the epilogue warps' own
+  // barrier, with a pair the relay's
+  const uint32_t acc_free = CG == 1 ? acce0 : acce0 + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 6);
   uint8_t* stage = smem + size_t(STAGES) * SS + 1024;  // 1024-byte aligned
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -455,6 +448,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf0 + 8 * b, 1);
       mbar_init(acce0 + 8 * b, kEpiWarps * CG);
+      if (CG == 2) mbar_init(acc_free + 8 * b, 1);
     }
     fence_mbar_init();
   }
@@ -493,7 +487,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       for (int kc = t.kc0; kc < t.kc1; ++kc, ++it) {
         const int st = it % STAGES;
         const uint32_t round = uint32_t(it / STAGES);
-        if (!wait_bar<CG>(empty0 + 8 * st, (round & 1u) ^ 1u)) timed_out = true;
+        if (!mbar_wait_bounded(empty0 + 8 * st, (round & 1u) ^ 1u)) timed_out = true;
         uint32_t fb = full0 + 8 * st;
         if (rank == 0) mbar_arrive_expect_tx(fb, tx);
         else fb = dsmem_map(fb, 0);
@@ -521,13 +515,13 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       int kc = t.kc0;
       do {  // one accumulator per segment (an empty K range still hands one over)
         const int b = tl & 1;
-        if (!wait_bar<CG>(acce0 + 8 * b, (uint32_t(tl >> 1) & 1u) ^ 1u)) timed_out = true;
+        if (!mbar_wait_bounded(acc_free + 8 * b, (uint32_t(tl >> 1) & 1u) ^ 1u)) timed_out = true;
         tc::fence_after_sync();
         const uint32_t d_tmem = tmem_base + uint32_t(b * 256);
         const int k1 = min(t.kc1, kc + SEG), kfirst = kc;
         for (; kc < k1; ++kc, ++it) {
           const int st = it % STAGES;
-          if (!wait_bar<CG>(full0 + 8 * st, uint32_t(it / STAGES) & 1u)) timed_out = true;
+          if (!mbar_wait_bounded(full0 + 8 * st, uint32_t(it / STAGES) & 1u)) timed_out = true;
           tc::fence_after_sync();
           const uint32_t sa = smem_u32(smem + size_t(st) * SS), sb = sa + SA;
 #pragma unroll
@@ -542,6 +536,25 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         ++tl;
       } while (kc < t.kc1);
     }
+  } else if (warp == kRelayWarp) {
+    // ---------------- relay: the epilogue warps of both CTAs hand an accumulator back at
+    // cluster scope.  Taking that in costs the MMA thread its queue (recipe rows, forward:
+    // 518 K cycles against 414 K); this thread does it and passes the news on in the CTA.
+    if (CG == 2 && lane == 0 && rank == 0) {
+      int tl = 0;
+      for (int w = tile0; w < W; w += tiles_step) {
+        const Item t = decode(wk, w, me, kch, ks);
+        int kc = t.kc0;
+        do {
+          const int b = tl & 1;
+          if (!mbar_wait_bounded(acce0 + 8 * b, uint32_t(tl >> 1) & 1u)) timed_out = true;
+          acquire_cluster(acce0 + 8 * b, uint32_t(tl >> 1) & 1u);
+          tc::mbar_arrive(acc_free + 8 * b);
+          ++tl;
+          kc += SEG;
+        } while (kc < t.kc1);
+      }
+    }
   } else if (warp >= 2) {
     // ---------------- epilogue: warp w reads TMEM lanes 32 * (w % 4) .. + 31 of its half
     // of the columns
@@ -551,9 +564,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     sh.sbuf = smem_u32(stage + (warp - 2) * staging_tiles(EPI) * 4096);
     sh.boxes = 0;
     sh.half = half, sh.n_valid = n_valid, sh.lane = lane;
-    // the forward's halves are even; the others' are whole 64-column boxes
-    const int first = EPI == kFwd ? bn / 2 : (bn / 64 + 1) / 2 * 64;
-    sh.c0 = half ? first : 0, sh.c1 = half ? bn : first;
+    sh.c0 = half * (bn / 2), sh.cols = bn / 2;
     auto release = [&](int b) {
       tc::fence_before_sync();
       __syncwarp();
@@ -574,13 +585,15 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           for (int i = 0; i < 128; ++i) z[i] = 0.f;
         for (int kc = t.kc0; kc < t.kc1; kc += SEG, ++tl) {
           const int b = tl & 1;
-          if (!wait_bar<CG>(accf0 + 8 * b, uint32_t(tl >> 1) & 1u)) timed_out = true;
+          if (!mbar_wait_bounded(accf0 + 8 * b, uint32_t(tl >> 1) & 1u)) timed_out = true;
           tc::fence_after_sync();
           const uint32_t taddr = tmem_base + lanes + uint32_t(b * 256 + sh.c0);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             float v[16];
+            __syncwarp();
             tmem_ld16(taddr + uint32_t(16 * c), v);
+            tmem_wait16(v);
 #pragma unroll
             for (int i = 0; i < 16; ++i) z[16 * c + i] += v[i];
           }
@@ -589,14 +602,15 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         fwd_finish(ea, sh, z);
       } else {
         const int b = tl & 1;
-        if (!wait_bar<CG>(accf0 + 8 * b, uint32_t(tl >> 1) & 1u)) timed_out = true;
+        if (!mbar_wait_bounded(accf0 + 8 * b, uint32_t(tl >> 1) & 1u)) timed_out = true;
         tc::fence_after_sync();
-        sh.taddr = tmem_base + lanes + uint32_t(b * 256);
-        if constexpr (EPI == kDz) dz_finish(ea, tmO, sh);
-        else if constexpr (EPI == kDh) f32_finish<true>(ea, tmO, sh);
-        else if constexpr (EPI == kDwF32) f32_finish<false>(ea, tmO, sh);
-        else bf16_finish(ea, tmO, sh);
+        // to registers at once, so that the next tile's MMAs have the accumulator early
+        float z[128];
+        tmem_ld128(tmem_base + lanes + uint32_t(b * 256 + sh.c0), z);
         release(b);
+        if constexpr (EPI == kDz) dz_finish(ea, tmO, sh, z);
+        else if constexpr (EPI == kDwBf16) bf16_finish(ea, tmO, sh, z);
+        else f32_finish<EPI>(ea, tmO, sh, z);
         ++tl;
       }
     }
@@ -631,11 +645,19 @@ __global__ void __launch_bounds__(kSlices * 32) merge_kernel(const View ws, cons
   const int i = r < pl.R ? ws.index[r] : -1;
   float m = -INFINITY, s = 0.f;
   if (i >= 0) {
-#pragma unroll 4
-    for (int64_t t = sl; t < 2 * pl.fwd_tiles; t += kSlices) {
-      const float2 p = ws.part[size_t(t) * pl.Rp + i];
-      const float nm = fmaxf(m, p.x), ref = nm == -INFINITY ? 0.f : nm;
-      s = s * ex2(m - ref) + p.y * ex2(p.x - ref);
+    constexpr int U = 8;  // pairs in flight
+    for (int64_t t = sl; t < 2 * pl.fwd_tiles; t += U * kSlices) {
+      float2 p[U];
+      float nm = m;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        p[u] = t + u * kSlices < 2 * pl.fwd_tiles ? ws.part[size_t(t + u * kSlices) * pl.Rp + i] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int u = 0; u < U; ++u) nm = fmaxf(nm, p[u].x);
+      const float ref = nm == -INFINITY ? 0.f : nm;
+      s *= ex2(m - ref);
+#pragma unroll
+      for (int u = 0; u < U; ++u) s += p[u].y * ex2(p[u].x - ref);
       m = nm;
     }
   }
@@ -745,22 +767,22 @@ int tiles(int64_t n, int64_t t) { return int(ceil_div(n, t)); }
 
 cudaError_t launch_fwd(const dspark_lce_problem_t& p, const dspark_lce_out_t& out, const Plan& pl, const View& ws,
                        cudaStream_t s) {
-  const int64_t ctas = std::min<int64_t>(ceil_div(p.R, 8), 4 * kSlots);
+  const int64_t ctas = std::min<int64_t>(p.R, 4 * kSlots);
   const int64_t rows_per_cta = ceil_div(p.R, ctas);
   prep_kernel<<<unsigned(ceil_div(p.R, rows_per_cta)), kPrepThreads, 0, s>>>(p, ws, out.num_tokens, rows_per_cta);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   CUtensorMap ma, mb;
   if (!tc::make_map(&ma, ws.hsup, pl.Rp, p.H, p.H, 64, kBM) ||
-      !tc::make_map(&mb, p.weight, p.V, p.H, p.weight_ld, 64, pl.bn_fwd / pl.cg))
+      !tc::make_map(&mb, p.weight, p.V, p.H, p.weight_ld, 64, kBN / pl.cg))
     return cudaErrorInvalidValue;
-  Work wk{tiles(p.R, kBM * pl.cg), tiles(p.V, pl.bn_fwd), tiles(p.H, BK), 16, 1, 0, &ws.hdr->n_valid};
+  Work wk{tiles(p.R, kBM * pl.cg), tiles(p.V, kBN), tiles(p.H, BK), 16, 1, 0, &ws.hdr->n_valid};
   EpiArgs ea{};
   ea.ws = ws;
   ea.plan = pl;
   ea.rows = int32_t(pl.Rp);
   ea.n_cols = int32_t(p.V);
-  if ((e = product<kFwd>(pl, ma, mb, ma, wk, ea, pl.bn_fwd, s)) != cudaSuccess) return e;
+  if ((e = product<kFwd>(pl, ma, mb, ma, wk, ea, kBN, s)) != cudaSuccess) return e;
   PdlLaunch l(pl.merge_blocks, kSlices * 32, 0, s);
   return cudaLaunchKernelEx(&l.cfg, merge_kernel, ws, pl, p.z_alpha, out);
 }
@@ -777,7 +799,7 @@ cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& 
     const int64_t ldz = pl.piece;
     const uint16_t* w0 = static_cast<const uint16_t*>(p.weight) + size_t(v0) * p.weight_ld;
     CUtensorMap w_k, w_mn, z_out, z_k, z_mn, o;
-    if (!tc::make_map(&w_k, w0, n, p.H, p.weight_ld, 64, pl.bn_dz / pl.cg) ||
+    if (!tc::make_map(&w_k, w0, n, p.H, p.weight_ld, 64, kBN / pl.cg) ||
         !make_out16_map(&z_out, ws.dz, pl.Rp, ldz, ldz))
       return cudaErrorInvalidValue;
     EpiArgs ea{};
@@ -788,17 +810,8 @@ cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& 
     ea.col0 = int32_t(v0);
     ea.z_alpha = p.z_alpha;
     ea.grad_scale = g.grad_scale;
-    const Work wz{tiles(p.R, kBM * pl.cg), tiles(n, pl.bn_dz), tiles(p.H, BK), 16, 1, 0, &ws.hdr->n_valid};
-    if ((e = product<kDz>(pl, h_k, w_k, z_out, wz, ea, pl.bn_dz, s)) != cudaSuccess) return e;
-    if (g.dhidden) {
-      if (!tc::make_map(&w_mn, w0, n, p.H, p.weight_ld, 64, 64) || !tc::make_map(&z_k, ws.dz, pl.Rp, ldz, ldz, 64, kBM) ||
-          !tc::make_out_map(&o, ws.planes, pl.plane_rows, p.H, p.H))
-        return cudaErrorInvalidValue;
-      ea.n_cols = int32_t(p.H);
-      ea.add = i > 0;
-      const Work wh{tiles(p.R, kBM * pl.cg), tiles(p.H, pl.bn_h), tiles(n, BK), 8, 1, 0, &ws.hdr->n_valid};
-      if ((e = product<kDh>(pl, z_k, w_mn, o, wh, ea, pl.bn_h, s)) != cudaSuccess) return e;
-    }
+    const Work wz{tiles(p.R, kBM * pl.cg), tiles(n, kBN), tiles(p.H, BK), 16, 1, 0, &ws.hdr->n_valid};
+    if ((e = product<kDz>(pl, h_k, w_k, z_out, wz, ea, kBN, s)) != cudaSuccess) return e;
     if (g.dweight) {
       void* d0 = static_cast<uint8_t*>(g.dweight) + size_t(v0) * g.dweight_ld * (f32 ? 4 : 2);
       if (!tc::make_map(&z_mn, ws.dz, pl.Rp, ldz, ldz, 64, 64) ||
@@ -811,6 +824,17 @@ cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& 
       e = f32 ? product<kDwF32>(pl, z_mn, h_mn, o, ww, ea, pl.bn_h, s)
               : product<kDwBf16>(pl, z_mn, h_mn, o, ww, ea, pl.bn_h, s);
       if (e != cudaSuccess) return e;
+    }
+    if (g.dhidden) {
+      if (!tc::make_map(&w_mn, w0, n, p.H, p.weight_ld, 64, 64) || !tc::make_map(&z_k, ws.dz, pl.Rp, ldz, ldz, 64, kBM) ||
+          !tc::make_out_map(&o, ws.planes, pl.plane_rows, p.H, p.H))
+        return cudaErrorInvalidValue;
+      // the sums last: the kernel after the last piece finds them in L2
+      ea.rows = int32_t(pl.Rp);
+      ea.n_cols = int32_t(p.H);
+      ea.add = i > 0;
+      const Work wh{tiles(p.R, kBM * pl.cg), tiles(p.H, pl.bn_h), tiles(n, BK), 8, 1, 0, &ws.hdr->n_valid};
+      if ((e = product<kDh>(pl, z_k, w_mn, o, wh, ea, pl.bn_h, s)) != cudaSuccess) return e;
     }
   }
   if (g.dhidden) {

@@ -7,6 +7,9 @@ namespace dspark {
 namespace lce {
 
 constexpr int kBM = 128;                             // tile rows per CTA (TMEM lanes)
+// Vocabulary columns per tile.  Narrower tiles (192, 208) that fill the last wave of tiles
+// better were measured no faster: on a pair of CTAs an MMA of N = 192 takes the time of 256.
+constexpr int kBN = 256;
 constexpr int kSlots = 148;                          // SMs the plan assumes
 constexpr size_t kPieceBytes = size_t(256) << 20;    // bound on the kept piece of dz
 constexpr int kMaxSplitTiles = 32;                   // more row tiles than this are not split
@@ -27,8 +30,6 @@ struct Plan {
   int64_t R, V, H;
   int64_t Rp;          // R rounded up to a whole 64-row K chunk
   int cg;              // CTAs per tile: 1, or a pair sharing one 256-row tile
-  int bn_fwd;          // vocabulary columns per tile of the forward product
-  int bn_dz;           // the same where dz is stored (whole 64-column boxes)
   int bn_h;            // hidden columns per tile of the gradient products
   int64_t fwd_tiles;   // vocabulary tiles of the forward product
   int64_t piece;       // vocabulary columns per piece of the backward
@@ -55,33 +56,18 @@ struct View {
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Columns per tile for `m` row tiles over n columns: the widest tile has the fewest operand
-// bytes per product, but the last wave of tiles over the SMs should be full.  `per` is the
-// step of widths the product can take.
-inline int pick_columns(int64_t m, int64_t n, int64_t slots, int per) {
-  int best = 256;
-  int64_t cost = INT64_MAX;
-  for (int bn = 256; bn >= 128; bn -= per) {
-    const int64_t c = ceil_div(m * ceil_div(n, bn), slots) * (bn + 8);  // 8: a tile's fixed part
-    if (c < cost) cost = c, best = bn;
-  }
-  return best;
-}
-
 inline Plan make_plan(int64_t R, int64_t V, int64_t H) {
   Plan p{};
   p.R = R, p.V = V, p.H = H;
   p.Rp = ceil_div(R, 64) * 64;
   p.cg = R > kBM ? 2 : 1;
   const int64_t slots = kSlots / p.cg, m_tiles = ceil_div(R, kBM * p.cg);
-  p.bn_fwd = pick_columns(m_tiles, V, slots, 16);
   p.bn_h = H > 128 ? 256 : 128;
-  p.fwd_tiles = ceil_div(V, p.bn_fwd);
+  p.fwd_tiles = ceil_div(V, kBN);
   const int64_t most = std::max<int64_t>(256, int64_t(kPieceBytes / (2 * size_t(p.Rp))) / 256 * 256);
   p.pieces = int(ceil_div(V, most));
   p.piece = ceil_div(ceil_div(V, p.pieces), 256) * 256;
   p.pieces = int(ceil_div(V, p.piece));
-  p.bn_dz = pick_columns(m_tiles, std::min(V, p.piece), slots, 64);
   // Few row and hidden tiles: the K range (the piece's vocabulary) is split so that the waves
   // of tiles over the SMs are full.  How many row tiles there are only the device knows (they
   // hold the labelled rows), so there is a number of splits for each count.
