@@ -17,7 +17,6 @@
 //   warp 0      one thread issues the TMA loads into a ring of 64-wide K stages
 //   warp 1      allocates TMEM; one thread (of the tile's first CTA) issues the MMAs
 //   warps 2..9  read the accumulator (a thread: one tile row, half the columns), finish it
-//   warp 10     (pair) passes on that both CTAs are done with an accumulator
 // The accumulator is double-buffered in TMEM: a tile's epilogue runs beside the next
 // tile's MMAs.
 #include <cuda_bf16.h>
@@ -34,8 +33,7 @@ namespace {
 
 using tc::BK;
 constexpr int kEpiWarps = 8;
-constexpr int kRelayWarp = 2 + kEpiWarps;
-constexpr int kThreads = 32 * (kRelayWarp + 1);
+constexpr int kThreads = 64 + 32 * kEpiWarps;
 
 // ------------------------------------------------------------------ prep
 // Each CTA takes a contiguous run of rows, counts the labelled rows before it (the labels
@@ -147,26 +145,34 @@ struct Work {
   int m_tiles, n_tiles, kchunks, group;
   int bound_m, bound_k;  // the number of labelled rows bounds the tile rows / the K range
   const int32_t* n_valid;
+  uint64_t span_inv, group_inv;  // ceil(2^64 / divisor): n / d = the high half of n * inverse
 };
+
+__host__ __device__ inline uint64_t inverse(uint32_t d) { return d == 1 ? 0 : ~uint64_t(0) / d + 1; }
+__device__ __forceinline__ int div_by(int n, uint64_t inv) { return inv == 0 ? n : int(__umul64hi(uint64_t(n), inv)); }
 
 struct Item {
   int mt, nt, s, kc0, kc1;
 };
 
+// (A division costs about a hundred cycles here, and the epilogue warps of short products
+// pass through this once per 2048 cycles: the common ones are multiplications.)
 __device__ __forceinline__ Item decode(const Work& wk, int w, int me, int kch, int ksplit) {
   Item it;
-  const int per = me * wk.n_tiles;
-  it.s = w / per;
-  int t = w - it.s * per;
-  const int span = wk.group * wk.n_tiles;
-  const int g = t / span;
-  t -= g * span;
-  const int m0 = g * wk.group;
-  const int gm = min(wk.group, me - m0);
-  it.nt = t / gm;
+  it.s = 0, it.kc0 = 0, it.kc1 = kch;
+  int t = w;
+  if (ksplit > 1) {
+    const int per = me * wk.n_tiles;
+    it.s = w / per;
+    t = w - it.s * per;
+    it.kc0 = int((int64_t(it.s) * kch) / ksplit);
+    it.kc1 = int((int64_t(it.s + 1) * kch) / ksplit);
+  }
+  const int g = div_by(t, wk.span_inv);
+  t -= g * wk.group * wk.n_tiles;
+  const int m0 = g * wk.group, gm = min(wk.group, me - m0);
+  it.nt = gm == wk.group ? div_by(t, wk.group_inv) : gm == 1 ? t : t / gm;
   it.mt = m0 + (t - it.nt * gm);
-  it.kc0 = int((int64_t(it.s) * kch) / ksplit);
-  it.kc1 = int((int64_t(it.s + 1) * kch) / ksplit);
   return it;
 }
 
@@ -181,14 +187,6 @@ struct EpiArgs {
   const float* grad_scale;
   int32_t add;               // dh: add to the planes; dw: add to dweight
 };
-
-// Acquire at cluster scope of a barrier phase already seen complete.
-__device__ __forceinline__ void acquire_cluster(uint32_t bar, uint32_t parity) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}"
-      ::"r"(bar), "r"(parity) : "memory");
-}
 
 // TMA tile load completing on the barrier of the tile's first CTA.
 template <int CG>
@@ -430,10 +428,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const uint32_t empty0 = full0 + 8 * STAGES;
   const uint32_t accf0 = empty0 + 8 * STAGES;
   const uint32_t acce0 = accf0 + 16;
-  // what the MMA thread waits on for an accumulator: with one CTA the epilogue warps' own
-  // barrier, with a pair the relay's
-  const uint32_t acc_free = CG == 1 ? acce0 : acce0 + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 6);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 4);
   uint8_t* stage = smem + size_t(STAGES) * SS + 1024;  // 1024-byte aligned
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -448,7 +443,6 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf0 + 8 * b, 1);
       mbar_init(acce0 + 8 * b, kEpiWarps * CG);
-      if (CG == 2) mbar_init(acc_free + 8 * b, 1);
     }
     fence_mbar_init();
   }
@@ -515,7 +509,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       int kc = t.kc0;
       do {  // one accumulator per segment (an empty K range still hands one over)
         const int b = tl & 1;
-        if (!mbar_wait_bounded(acc_free + 8 * b, (uint32_t(tl >> 1) & 1u) ^ 1u)) timed_out = true;
+        if (!mbar_wait_bounded(acce0 + 8 * b, (uint32_t(tl >> 1) & 1u) ^ 1u)) timed_out = true;
         tc::fence_after_sync();
         const uint32_t d_tmem = tmem_base + uint32_t(b * 256);
         const int k1 = min(t.kc1, kc + SEG), kfirst = kc;
@@ -536,25 +530,6 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         ++tl;
       } while (kc < t.kc1);
     }
-  } else if (warp == kRelayWarp) {
-    // ---------------- relay: the epilogue warps of both CTAs hand an accumulator back at
-    // cluster scope.  Taking that in costs the MMA thread its queue (recipe rows, forward:
-    // 518 K cycles against 414 K); this thread does it and passes the news on in the CTA.
-    if (CG == 2 && lane == 0 && rank == 0) {
-      int tl = 0;
-      for (int w = tile0; w < W; w += tiles_step) {
-        const Item t = decode(wk, w, me, kch, ks);
-        int kc = t.kc0;
-        do {
-          const int b = tl & 1;
-          if (!mbar_wait_bounded(acce0 + 8 * b, uint32_t(tl >> 1) & 1u)) timed_out = true;
-          acquire_cluster(acce0 + 8 * b, uint32_t(tl >> 1) & 1u);
-          tc::mbar_arrive(acc_free + 8 * b);
-          ++tl;
-          kc += SEG;
-        } while (kc < t.kc1);
-      }
-    }
   } else if (warp >= 2) {
     // ---------------- epilogue: warp w reads TMEM lanes 32 * (w % 4) .. + 31 of its half
     // of the columns
@@ -565,12 +540,17 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     sh.boxes = 0;
     sh.half = half, sh.n_valid = n_valid, sh.lane = lane;
     sh.c0 = half * (bn / 2), sh.cols = bn / 2;
+    // Hands an accumulator back to the MMA thread.  What is ordered is TMEM, by the loads'
+    // wait and the tcgen05 fences on both sides of the barrier, and no other memory: the
+    // barrier operations stay at CTA scope also between the pair (a cluster-scope release
+    // waits for this thread's stores, 1300 cycles a tile; a cluster-scope acquire empties
+    // the MMA thread's queue).
     auto release = [&](int b) {
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) {
         if (rank == 0) tc::mbar_arrive(acce0 + 8 * b);
-        else asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+        else asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];"
                           ::"r"(dsmem_map(acce0 + 8 * b, 0)) : "memory");
       }
     };
@@ -763,6 +743,12 @@ cudaError_t product(const Plan& pl, const CUtensorMap& a, const CUtensorMap& b, 
 
 int tiles(int64_t n, int64_t t) { return int(ceil_div(n, t)); }
 
+// `over_rows`: the labelled rows are the K range (else the tile rows).
+Work make_work(int m_tiles, int n_tiles, int kchunks, int group, bool over_rows, const View& ws) {
+  return Work{m_tiles, n_tiles, kchunks, group, !over_rows, over_rows, &ws.hdr->n_valid,
+              inverse(uint32_t(group) * uint32_t(n_tiles)), inverse(uint32_t(group))};
+}
+
 }  // namespace
 
 cudaError_t launch_fwd(const dspark_lce_problem_t& p, const dspark_lce_out_t& out, const Plan& pl, const View& ws,
@@ -776,7 +762,7 @@ cudaError_t launch_fwd(const dspark_lce_problem_t& p, const dspark_lce_out_t& ou
   if (!tc::make_map(&ma, ws.hsup, pl.Rp, p.H, p.H, 64, kBM) ||
       !tc::make_map(&mb, p.weight, p.V, p.H, p.weight_ld, 64, kBN / pl.cg))
     return cudaErrorInvalidValue;
-  Work wk{tiles(p.R, kBM * pl.cg), tiles(p.V, kBN), tiles(p.H, BK), 16, 1, 0, &ws.hdr->n_valid};
+  const Work wk = make_work(tiles(p.R, kBM * pl.cg), tiles(p.V, kBN), tiles(p.H, BK), 16, false, ws);
   EpiArgs ea{};
   ea.ws = ws;
   ea.plan = pl;
@@ -810,7 +796,7 @@ cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& 
     ea.col0 = int32_t(v0);
     ea.z_alpha = p.z_alpha;
     ea.grad_scale = g.grad_scale;
-    const Work wz{tiles(p.R, kBM * pl.cg), tiles(n, kBN), tiles(p.H, BK), 16, 1, 0, &ws.hdr->n_valid};
+    const Work wz = make_work(tiles(p.R, kBM * pl.cg), tiles(n, kBN), tiles(p.H, BK), 16, false, ws);
     if ((e = product<kDz>(pl, h_k, w_k, z_out, wz, ea, kBN, s)) != cudaSuccess) return e;
     if (g.dweight) {
       void* d0 = static_cast<uint8_t*>(g.dweight) + size_t(v0) * g.dweight_ld * (f32 ? 4 : 2);
@@ -820,7 +806,7 @@ cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& 
       ea.rows = int32_t(n);
       ea.n_cols = int32_t(p.H);
       ea.add = g.accumulate ? 1 : 0;
-      const Work ww{tiles(n, kBM * pl.cg), tiles(p.H, pl.bn_h), tiles(p.R, BK), 1, 0, 1, &ws.hdr->n_valid};
+      const Work ww = make_work(tiles(n, kBM * pl.cg), tiles(p.H, pl.bn_h), tiles(p.R, BK), 1, true, ws);
       e = f32 ? product<kDwF32>(pl, z_mn, h_mn, o, ww, ea, pl.bn_h, s)
               : product<kDwBf16>(pl, z_mn, h_mn, o, ww, ea, pl.bn_h, s);
       if (e != cudaSuccess) return e;
@@ -833,7 +819,7 @@ cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& 
       ea.rows = int32_t(pl.Rp);
       ea.n_cols = int32_t(p.H);
       ea.add = i > 0;
-      const Work wh{tiles(p.R, kBM * pl.cg), tiles(p.H, pl.bn_h), tiles(n, BK), 8, 1, 0, &ws.hdr->n_valid};
+      const Work wh = make_work(tiles(p.R, kBM * pl.cg), tiles(p.H, pl.bn_h), tiles(n, BK), 8, false, ws);
       if ((e = product<kDh>(pl, z_k, w_mn, o, wh, ea, pl.bn_h, s)) != cudaSuccess) return e;
     }
   }
