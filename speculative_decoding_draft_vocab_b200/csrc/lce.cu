@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const dspark_lce_pro
 struct Work {
   int m_tiles, n_tiles, kchunks, group;
   int bound_m, bound_k;  // the number of labelled rows bounds the tile rows / the K range
+  int beside;            // runs beside the kernel launched before it
   const int32_t* n_valid;
   uint64_t span_inv, group_inv;  // ceil(2^64 / divisor): n / d = the high half of n * inverse
 };
@@ -187,6 +188,10 @@ struct EpiArgs {
   const float* grad_scale;
   int32_t add;               // dh: add to the planes; dw: add to dweight
 };
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 
 // TMA tile load completing on the barrier of the tile's first CTA.
 template <int CG>
@@ -446,7 +451,13 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     }
     fence_mbar_init();
   }
+  if (threadIdx.x == 32) {  // fetched while the kernel before this one runs
+    prefetch_map(&tmA);
+    prefetch_map(&tmB);
+    prefetch_map(&tmO);
+  }
   if (warp == 1) {
+    __syncwarp();
     if constexpr (CG == 1) {
       tc::tmem_alloc(smem_u32(tmem_slot), 512);
     } else {
@@ -460,7 +471,10 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   else cluster_sync();
   tc::fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
-  pdl_wait();  // what the kernel before it wrote
+  // What the kernel before it wrote.  The hidden gradient may run beside the head gradient
+  // launched before it (`beside`): that one let it start only once it had dz itself; it is
+  // waited for at the end, so that what follows finds both done.
+  if (!wk.beside) pdl_wait();
   pdl_trigger();
 
   const int n_valid = *wk.n_valid;
@@ -597,6 +611,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     if (lane == 0) tc::bulk_wait_read<0>();  // the staging stays until the TMA engine has read it
   }
   if (timed_out) atomicOr(&ea.ws.hdr->status, kFlagTimeout);
+  if (wk.beside) pdl_wait();
   tc::fence_before_sync();
   if constexpr (CG == 1) __syncthreads();
   else cluster_sync();  // the pair's barriers and TMEM stay until both are done
@@ -609,7 +624,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 
 // ------------------------------------------------------------------ merge
 // 32 rows per CTA, the tiles of a row spread over 32 slices (one warp each, the rows its
-// lanes); the slices' pairs are combined in slice order.  Loss terms in FP64, summed per
+// lanes); then a warp per row combines the slices' pairs.  Loss terms in FP64, summed per
 // CTA and by the last CTA in CTA order: a fixed order, so repeated calls agree bit by bit.
 constexpr int kSlices = 32;
 
@@ -643,32 +658,46 @@ __global__ void __launch_bounds__(kSlices * 32) merge_kernel(const View ws, cons
   }
   sp[sl][lane] = make_float2(m, s);
   __syncthreads();
-  if (sl == 0) {
-    double term = 0.0;
+  // now warp = row, lane = slice: a fixed tree over the slices
+  const int64_t row = int64_t(blockIdx.x) * kMergeRows + sl;
+  const int k = row < pl.R ? ws.index[row] : -1;
+  const float2 p = sp[lane][sl];
+  m = p.x;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  s = p.y * ex2(p.x - (m == -INFINITY ? 0.f : m));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if (lane == 0) {
     float ce = 0.f, lse = 0.f;
-    if (i >= 0) {
-      for (int k = 1; k < kSlices; ++k) {
-        const float2 p = sp[k][lane];
-        const float nm = fmaxf(m, p.x), ref = nm == -INFINITY ? 0.f : nm;
-        s = s * ex2(m - ref) + p.y * ex2(p.x - ref);
-        m = nm;
-      }
+    double term = 0.0;
+    if (k >= 0) {
       const float lse2 = m + log2f(s);
-      ws.lse2[i] = lse2;
+      ws.lse2[k] = lse2;
       lse = lse2 * kLn2;
-      ce = fmaf(lse2, kLn2, -ws.zt[i]);
-      term = double(ws.w[i]) * (double(ce) + double(z_alpha) * double(lse) * double(lse));
+      ce = fmaf(lse2, kLn2, -ws.zt[k]);
+      term = double(ws.w[k]) * (double(ce) + double(z_alpha) * double(lse) * double(lse));
     }
-    if (r < pl.R) {
-      if (out.ce_rows) out.ce_rows[r] = ce;
-      if (out.lse_rows) out.lse_rows[r] = lse;
+    if (row < pl.R) {
+      if (out.ce_rows) out.ce_rows[row] = ce;
+      if (out.lse_rows) out.lse_rows[row] = lse;
     }
+    sd[sl] = term;
+  }
+  __syncthreads();
+  if (sl == 0) {
+    double term = sd[lane];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) term += __shfl_xor_sync(0xffffffffu, term, off);
     if (lane == 0) {
-      ws.loss_part[blockIdx.x] = term;
-      __threadfence();
-      is_last = atomicAdd(&ws.hdr->done, 1u) == gridDim.x - 1;
+      if (gridDim.x == 1) {  // nothing to add up
+        if (out.loss_num) *out.loss_num = float(term);
+        is_last = 0;
+      } else {
+        ws.loss_part[blockIdx.x] = term;
+        __threadfence();
+        is_last = atomicAdd(&ws.hdr->done, 1u) == gridDim.x - 1;
+      }
     }
   }
   __syncthreads();
@@ -745,7 +774,7 @@ int tiles(int64_t n, int64_t t) { return int(ceil_div(n, t)); }
 
 // `over_rows`: the labelled rows are the K range (else the tile rows).
 Work make_work(int m_tiles, int n_tiles, int kchunks, int group, bool over_rows, const View& ws) {
-  return Work{m_tiles, n_tiles, kchunks, group, !over_rows, over_rows, &ws.hdr->n_valid,
+  return Work{m_tiles, n_tiles, kchunks, group, !over_rows, over_rows, 0, &ws.hdr->n_valid,
               inverse(uint32_t(group) * uint32_t(n_tiles)), inverse(uint32_t(group))};
 }
 
@@ -755,8 +784,9 @@ cudaError_t launch_fwd(const dspark_lce_problem_t& p, const dspark_lce_out_t& ou
                        cudaStream_t s) {
   const int64_t ctas = std::min<int64_t>(p.R, 4 * kSlots);
   const int64_t rows_per_cta = ceil_div(p.R, ctas);
-  prep_kernel<<<unsigned(ceil_div(p.R, rows_per_cta)), kPrepThreads, 0, s>>>(p, ws, out.num_tokens, rows_per_cta);
-  cudaError_t e = cudaGetLastError();
+  PdlLaunch first(ceil_div(p.R, rows_per_cta), kPrepThreads, 0, s);
+  first.cfg.numAttrs = 0;  // the first kernel of the call waits for all work before it
+  cudaError_t e = cudaLaunchKernelEx(&first.cfg, prep_kernel, p, ws, out.num_tokens, rows_per_cta);
   if (e != cudaSuccess) return e;
   CUtensorMap ma, mb;
   if (!tc::make_map(&ma, ws.hsup, pl.Rp, p.H, p.H, 64, kBM) ||
@@ -819,7 +849,8 @@ cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& 
       ea.rows = int32_t(pl.Rp);
       ea.n_cols = int32_t(p.H);
       ea.add = i > 0;
-      const Work wh = make_work(tiles(p.R, kBM * pl.cg), tiles(p.H, pl.bn_h), tiles(n, BK), 8, false, ws);
+      Work wh = make_work(tiles(p.R, kBM * pl.cg), tiles(p.H, pl.bn_h), tiles(n, BK), 8, false, ws);
+      wh.beside = g.dweight != nullptr;
       if ((e = product<kDh>(pl, z_k, w_mn, o, wh, ea, pl.bn_h, s)) != cudaSuccess) return e;
     }
   }

@@ -113,7 +113,7 @@ cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t s);
 // ------------------------------------------------------------------ gradient clipping
 namespace clip {
 
-constexpr int kMaxTensors = 500;   // descriptors per launch (kernel parameters)
+constexpr int kMaxTensors = 900;   // descriptors per launch (kernel parameters)
 constexpr int kGrid = 148 * 8;     // CTAs of a launch, at most
 constexpr int kThreads = 256;
 constexpr int64_t kChunk = 8192;   // elements a CTA takes at a time

@@ -436,11 +436,14 @@ class _DeviceCall:
         self.ws_ptr, self.ws_len = _aligned_ws(self.ws)
 
     def _run(self, fn, where, stream, *args) -> None:
-        if torch.cuda.current_device() != self.device.index:
+        index = self.device.index
+        if torch.cuda.current_device() != index:
             with torch.cuda.device(self.device):
                 return self._run(fn, where, stream, *args)
-        s = torch.cuda.current_stream().cuda_stream if stream is None else stream
-        abi.check(fn(*args, ctypes.c_void_p(s)), where)
+        s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream
+        status = fn(*args, s)
+        if status:
+            abi.check(status, where)
 
     def check_status(self, stream=None) -> int:
         with torch.cuda.device(self.device):
@@ -514,19 +517,19 @@ class LinearCE(_DeviceCall):
         o.loss_num, o.num_tokens = _ptr(self.loss_num), _ptr(self.num_tokens)
         o.ce_rows, o.lse_rows = _ptr(self.ce_rows), _ptr(self.lse_rows)
         self.out = o
-        self._workspace(int(abi.dspark_lce_workspace_size(
-            ctypes.byref(p), ctypes.byref(self.grads) if self.grads is not None else None)))
+        grads = ctypes.byref(self.grads) if self.grads is not None else None
+        self._workspace(int(abi.dspark_lce_workspace_size(ctypes.byref(p), grads)))
+        self._fwd_args = (ctypes.byref(p), ctypes.byref(o), self.ws_ptr, self.ws_len)
+        self._bwd_args = (ctypes.byref(p), grads, self.ws_ptr, self.ws_len)
 
     def forward(self, stream=None) -> None:
-        self._run(abi.dspark_lce_fwd, "dspark_lce_fwd", stream, ctypes.byref(self.prob), ctypes.byref(self.out),
-                  self.ws_ptr, self.ws_len)
+        self._run(abi.dspark_lce_fwd, "dspark_lce_fwd", stream, *self._fwd_args)
 
     def backward(self, stream=None) -> None:
         """The gradients of the last forward(), times ``grad_scale``."""
         if self.grads is None:
             raise ValueError("this call was built without gradients")
-        self._run(abi.dspark_lce_bwd, "dspark_lce_bwd", stream, ctypes.byref(self.prob), ctypes.byref(self.grads),
-                  self.ws_ptr, self.ws_len)
+        self._run(abi.dspark_lce_bwd, "dspark_lce_bwd", stream, *self._bwd_args)
 
 
 class _EmbedCall(_DeviceCall):
@@ -626,11 +629,11 @@ class GradClip(_DeviceCall):
         self.coef = torch.ones(1, dtype=torch.float32, device=self.device)
         self.sumsq = torch.zeros(1, dtype=torch.float64, device=self.device)
         self._workspace(int(abi.dspark_grad_workspace_size(self.count)))
+        self._tail = (self.max_norm, _ptr(self.norm), _ptr(self.coef), self.ws_ptr, self.ws_len)
 
     def launch(self, stream=None) -> None:
-        tail = (self.max_norm, _ptr(self.norm), _ptr(self.coef), self.ws_ptr, self.ws_len)
         if self.group is None:
-            self._run(abi.dspark_grad_clip, "dspark_grad_clip", stream, self.tensors, self.count, *tail)
+            self._run(abi.dspark_grad_clip, "dspark_grad_clip", stream, self.tensors, self.count, *self._tail)
             return
         import torch.distributed as dist
         if stream is not None:
@@ -638,4 +641,5 @@ class GradClip(_DeviceCall):
         self._run(abi.dspark_grad_sumsq, "dspark_grad_sumsq", None, self.tensors, self.count, _ptr(self.sumsq),
                   self.ws_ptr, self.ws_len)
         dist.all_reduce(self.sumsq, op=dist.ReduceOp.SUM, group=self.group)
-        self._run(abi.dspark_grad_scale, "dspark_grad_scale", None, self.tensors, self.count, _ptr(self.sumsq), *tail)
+        self._run(abi.dspark_grad_scale, "dspark_grad_scale", None, self.tensors, self.count, _ptr(self.sumsq),
+                  *self._tail)
