@@ -112,19 +112,22 @@ __global__ void __launch_bounds__(256, 8) lookup_kernel(const FwdArgs a) {
 // ------------------------------------------------------------------ zero rows
 // The table rows that no id touches.  While the ids are sorted, what is touched is not known
 // and the memory is idle: the sorting kernels' spare CTAs zero the first plan.fill rows
-// whatever their ids (a touched one is written again later); the two kernels after the sort
-// zero the others beside their sums, looking each row up in the sorted keys.
+// whatever their ids (a touched one is written again later); the sums' kernel zeroes the
+// others, looking each row up in the sorted keys.  (8192 rows, table 151936 x 256 FP32: all
+// rows beside the sort 45.5 us, all beside the sums 53.9, 64 MB beside the sort 41.4; a share
+// beside the joins as well 45.5.)  The zeros are streamed past L2, which holds the keys and
+// the partial sums.
 template <bool TF32>
 __device__ void zero_rows(const BwdArgs& a, int64_t r0, int64_t r1, int64_t thread, int64_t threads) {
   constexpr int N = Vec<TF32>::N;
   const int64_t nv = a.p.D / N, ldv = a.dtable_ld / N;
   uint4* t = static_cast<uint4*>(a.dtable);
   if (ldv == nv) {
-    for (int64_t i = r0 * nv + thread; i < r1 * nv; i += threads) t[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int64_t i = r0 * nv + thread; i < r1 * nv; i += threads) __stcs(t + i, make_uint4(0u, 0u, 0u, 0u));
   } else {
     for (int64_t i = thread; i < (r1 - r0) * nv; i += threads) {
       const int64_t r = i / nv;
-      t[(r0 + r) * ldv + (i - r * nv)] = make_uint4(0u, 0u, 0u, 0u);
+      __stcs(t + (r0 + r) * ldv + (i - r * nv), make_uint4(0u, 0u, 0u, 0u));
     }
   }
 }
@@ -171,7 +174,73 @@ __device__ __forceinline__ void warp_ranks(const uint32_t (&digit)[ITEMS], uint1
   }
 }
 
-// Up to kSmallRows rows: one cluster of eight CTAs keeps them in registers, one, two or four
+// Up to kRankRows rows: a row's place is the number of rows before it in the order, and
+// every row can count that for itself.  kRankThreads / 32 warps each take a stretch of the keys
+// (in shared memory, four to a load) for the CTA's 32 rows, one per lane.  R^2 comparisons,
+// spread over the whole GPU and without any exchange (the gradient of 448 rows into a table of
+// 256 columns takes 10.2 us so, 17.4 with the cluster's sort; of 4096 rows 14.3 and 20.1; of
+// 8192 rows 24.5 and 23.2); the other CTAs zero table rows meanwhile.
+__global__ void __launch_bounds__(kRankThreads) rank_kernel(const BwdArgs a) {
+  pdl_trigger();
+  const int R = int(a.p.R), ranking = (R + 31) / 32;
+  if (int(blockIdx.x) >= ranking) {
+    zero_share(a, 0, 1, int(blockIdx.x) - ranking, int(gridDim.x) - ranking);
+    return;
+  }
+  extern __shared__ uint4 smem_rank[];
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem_rank);  // R rounded up to 4, then the counts
+  constexpr int kWarps = kRankThreads / 32;
+  __shared__ uint32_t count[kWarps][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  bool bad = false;
+  const int padded = (R + 3) / 4 * 4;
+#pragma unroll 8
+  for (int i = tid; i < padded; i += kRankThreads) keys[i] = i < R ? key_of(a, i, bad) : ~0u;
+  const int any_bad = __syncthreads_or(bad);
+  if (blockIdx.x == 0 && tid == 0) a.ws.hdr->status = any_bad ? kFlagIdOutOfRange : 0u;
+  const int row = int(blockIdx.x) * 32 + lane;
+  const uint32_t key = row < R ? keys[row] : 0u;
+  // before row: every earlier row with a key not above, every later one with a key below
+  const int quads = padded / 4, per = (quads + kWarps - 1) / kWarps;
+  const int q0 = warp * per, q1 = min(q0 + per, quads);
+  const int own = int(blockIdx.x) * 8;  // the quads [own, own + 8) hold the CTA's rows themselves
+  uint32_t n = 0;
+  const uint32_t upto = key + 1;  // (keys are at most 2^30)
+#pragma unroll 8
+  for (int q = q0; q < min(q1, own); ++q) {
+    const uint4 k = reinterpret_cast<const uint4*>(keys)[q];
+    n += (k.x < upto) + (k.y < upto) + (k.z < upto) + (k.w < upto);
+  }
+  for (int q = max(q0, own); q < min(q1, own + 8); ++q) {
+    const uint4 k = reinterpret_cast<const uint4*>(keys)[q];
+    n += (k.x < key + (4 * q < row)) + (k.y < key + (4 * q + 1 < row)) + (k.z < key + (4 * q + 2 < row)) +
+         (k.w < key + (4 * q + 3 < row));
+  }
+#pragma unroll 8
+  for (int q = max(q0, own + 8); q < q1; ++q) {
+    const uint4 k = reinterpret_cast<const uint4*>(keys)[q];
+    n += (k.x < key) + (k.y < key) + (k.z < key) + (k.w < key);
+  }
+  count[warp][lane] = n;
+  __syncthreads();
+  if (warp == 0 && row < R) {
+    uint32_t at = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) at += count[w][lane];
+    a.ws.key[0][at] = key;
+    a.ws.row[0][at] = uint32_t(row);
+  }
+}
+
+cudaError_t rank_sort(const BwdArgs& a, cudaStream_t s) {
+  const size_t smem = size_t(a.p.R + 3) / 4 * 16;
+  const int spare = fill_ctas(a.plan, a.p.D * (a.table_f32 ? 4 : 2), 1, 148 * 4);
+  PdlLaunch l((a.p.R + 31) / 32 + spare, kRankThreads, smem, s);
+  l.cfg.numAttrs = 0;  // the first kernel of the call waits for all work before it
+  return cudaLaunchKernelEx(&l.cfg, rank_kernel, a);
+}
+
+// More rows, up to kSmallRows: one cluster of eight CTAs keeps them in registers, one, two or four
 // per thread, and moves them through its distributed shared memory; the other clusters zero
 // table rows meanwhile.  (8192 rows: 20 us in one CTA, whose issue slots the ranking fills.)
 struct SmallSort {
@@ -282,13 +351,14 @@ cudaError_t small_sort(const BwdArgs& a, cudaStream_t s) {
   auto kern = small_sort_kernel<ITEMS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(SmallSort)));
   if (e != cudaSuccess) return e;
-  const int spare = a.plan.fill > 0 ? 148 * 2 / kSmallCtas * kSmallCtas : 0;
+  const int spare =
+      (fill_ctas(a.plan, a.p.D * (a.table_f32 ? 4 : 2), 1, 148 * 2) + kSmallCtas - 1) / kSmallCtas * kSmallCtas;
   PdlLaunch l(kSmallCtas + spare, kSmallThreads, sizeof(SmallSort), s, kSmallCtas);
   l.at[0].val.programmaticStreamSerializationAllowed = 0;  // the first kernel of the call waits for all work before it
   return cudaLaunchKernelEx(&l.cfg, kern, a);
 }
 
-// More rows: a pass is two kernels.  Each CTA counts the digits of its run of rows; then each
+// Still more rows: a pass is two kernels.  Each CTA counts the digits of its run of rows; then each
 // CTA finds where its rows of each digit go (all smaller digits, the same digit in the CTAs
 // before it) and moves them in order.  The first pass reads the ids themselves.
 struct Pass {
@@ -457,7 +527,7 @@ __device__ void zero_untouched(const BwdArgs& a, const uint32_t* key, int64_t r0
   uint4* t = static_cast<uint4*>(a.dtable);
   for (uint32_t m = free; m != 0; m &= m - 1) {
     uint4* d = t + (r0 + __ffs(m) - 1) * ldv;
-    for (int64_t j = lane; j < nv; j += 32) d[j] = make_uint4(0u, 0u, 0u, 0u);
+    for (int64_t j = lane; j < nv; j += 32) __stcs(d + j, make_uint4(0u, 0u, 0u, 0u));
   }
 }
 
@@ -475,7 +545,7 @@ __global__ void __launch_bounds__(256) sum_kernel(const BwdArgs a, const uint32_
   const int64_t w = int64_t(blockIdx.x) * 8 + threadIdx.x / 32;
   if (w >= a.plan.windows * blocks) {
     const int64_t r0 = a.plan.fill + (w - a.plan.windows * blocks) * 32;
-    if (r0 < a.plan.fill_sum) zero_untouched<TF32>(a, key, r0, a.plan.fill_sum, lane);
+    if (!a.accumulate && r0 < a.p.Vt) zero_untouched<TF32>(a, key, r0, a.p.Vt, lane);
     return;
   }
   const int64_t win = w / blocks, j = (w - win * blocks) * 32 + lane;
@@ -533,20 +603,16 @@ __global__ void __launch_bounds__(256) sum_kernel(const BwdArgs a, const uint32_
 }
 
 // The segments that cross windows: the window a segment begins in adds the parts that the
-// windows after it left.  Warps past the windows zero untouched table rows.
+// windows after it left.
 template <bool F32, bool TF32>
 __global__ void __launch_bounds__(256) join_kernel(const BwdArgs a, const uint32_t* key) {
   pdl_wait();
   pdl_trigger();
-  constexpr int N = Vec<F32>::N, U = F32 ? 16 : 8;  // parts in flight
+  constexpr int N = Vec<F32>::N, U = F32 ? 32 : 16;  // parts in flight
   const int lane = threadIdx.x & 31;
   const int64_t nv = a.p.D / N, blocks = (nv + 31) / 32;
   const int64_t w = int64_t(blockIdx.x) * 8 + threadIdx.x / 32;
-  if (w >= a.plan.windows * blocks) {
-    const int64_t r0 = a.plan.fill_sum + (w - a.plan.windows * blocks) * 32;
-    if (!a.accumulate && r0 < a.p.Vt) zero_untouched<TF32>(a, key, r0, a.p.Vt, lane);
-    return;
-  }
+  if (w >= a.plan.windows * blocks) return;
   const int64_t win = w / blocks, j = (w - win * blocks) * 32 + lane;
   const int64_t p0 = win * a.plan.window, p1 = p0 + a.plan.window;
   if (p1 >= a.p.R) return;
@@ -586,12 +652,11 @@ __global__ void __launch_bounds__(256) join_kernel(const BwdArgs a, const uint32
 template <bool F32, bool TF32>
 cudaError_t sums(const BwdArgs& a, const uint32_t* key, const uint32_t* row, cudaStream_t s) {
   const int64_t nv = a.p.D / Vec<F32>::N, warps = a.plan.windows * ((nv + 31) / 32);
-  const int64_t in_sum = (a.plan.fill_sum - a.plan.fill + 31) / 32;
-  const int64_t in_join = a.accumulate ? 0 : (a.p.Vt - a.plan.fill_sum + 31) / 32;
-  PdlLaunch l((warps + in_sum + 7) / 8, 256, 0, s);
+  const int64_t zeros = a.accumulate ? 0 : (a.p.Vt - a.plan.fill + 31) / 32;
+  PdlLaunch l((warps + zeros + 7) / 8, 256, 0, s);
   cudaError_t e = cudaLaunchKernelEx(&l.cfg, sum_kernel<F32, TF32>, a, key, row);
   if (e != cudaSuccess) return e;
-  PdlLaunch l2((warps + in_join + 7) / 8, 256, 0, s);
+  PdlLaunch l2((warps + 7) / 8, 256, 0, s);
   return cudaLaunchKernelEx(&l2.cfg, join_kernel<F32, TF32>, a, key);
 }
 
@@ -609,13 +674,15 @@ cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t s) {
 cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t s) {
   cudaError_t e;
   int from = 0;
-  if (a.p.R <= kSmallRows) {
+  if (a.p.R <= kRankRows) {
+    if ((e = rank_sort(a, s)) != cudaSuccess) return e;
+  } else if (a.p.R <= kSmallRows) {
     e = a.p.R <= kSmallRows / 4   ? small_sort<kSmallItems / 4>(a, s)
         : a.p.R <= kSmallRows / 2 ? small_sort<kSmallItems / 2>(a, s)
                                   : small_sort<kSmallItems>(a, s);
     if (e != cudaSuccess) return e;
   } else {
-    const int spare = a.plan.fill > 0 ? 148 * 3 : 0;
+    const int spare = fill_ctas(a.plan, a.p.D * (a.table_f32 ? 4 : 2), 2 * a.plan.passes, 148 * 3);
     for (int k = 0; k < a.plan.passes; ++k) {
       const Pass ps{k * kDigitBits, k, a.ws.key[from], a.ws.row[from], a.ws.key[1 - from], a.ws.row[1 - from]};
       PdlLaunch l(a.plan.ctas + spare, kSortThreads, 0, s);

@@ -11,6 +11,8 @@ constexpr int kSortThreads = 512;
 constexpr int kSortItems = 2;                          // per thread and chunk
 constexpr int kSortChunk = kSortThreads * kSortItems;  // rows ranked at a time
 constexpr int kSortCtas = 128;                         // at most: a CTA sorts a run of chunks
+constexpr int kRankThreads = 512;
+constexpr int kRankRows = 4096;                        // placed by counting
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallItems = 4;                         // rows per thread, at most
 constexpr int kSmallCtas = 8;
@@ -31,8 +33,7 @@ struct Plan {
   int ctas;            // sorting CTAs
   int window;          // sorted rows per partial sum
   int64_t windows;
-  int64_t fill;        // table rows [0, fill) are zeroed beside the sort (0 when accumulating),
-  int64_t fill_sum;    // [fill, fill_sum) beside the windows' sums, the others beside the joins
+  int64_t fill;        // table rows [0, fill) are zeroed beside the sort (0 when accumulating)
 };
 
 inline Plan make_plan(int64_t R, int64_t Vt, int64_t D, bool f32) {
@@ -44,22 +45,26 @@ inline Plan make_plan(int64_t R, int64_t Vt, int64_t D, bool f32) {
   const int64_t chunks = (R + kSortChunk - 1) / kSortChunk;
   p.run = (chunks + kSortCtas - 1) / kSortCtas * kSortChunk;
   p.ctas = int((R + p.run - 1) / p.run);
-  // windows of 16 to 512 sorted rows: as long as 32 warps per SM still have one each
-  const int64_t cols = f32 ? 128 : 256, blocks = (D + cols - 1) / cols;
-  p.window = 16;
+  // windows of 16 to 512 sorted rows: longer ones as long as 32 warps per SM still have one
+  // each (32749 rows of 4096 columns: 64 rows 128 us, 256 rows 200 us).  Beyond 16384 rows at
+  // least 32, for the sake of the segments that cross windows (131072 rows of 256 columns:
+  // 16 rows 175 us, 32 rows 118 us)
+  const int64_t cols = f32 ? 128 : 256, blocks = (D + cols - 1) / cols;  // a warp's columns
+  p.window = R > 16384 ? 32 : 16;
   while (p.window < 512 && (R / (2 * p.window)) * blocks >= 148 * 32) p.window *= 2;
   p.windows = (R + p.window - 1) / p.window;
   return p;
 }
 
-// How the zeroing of the table's rows is spread over the kernels of the call: what fits the
-// time each spends waiting for latencies, the bulk beside the sums.
-inline void plan_fill(Plan& p, int64_t row_bytes) {
-  const double sort = p.R <= kSmallRows ? 64e6 : 24e6 * 2 * p.passes, join = 32e6;
-  const double total = double(p.Vt) * double(row_bytes);
-  const double f = total < sort + join ? total / (sort + join) : 1.0;
-  p.fill = int64_t(f * sort / double(row_bytes));
-  p.fill_sum = std::max(p.fill, p.Vt - int64_t(f * join / double(row_bytes)));
+// Table rows zeroed beside the sort: as many as its kernels' latencies hide.
+inline int64_t fill_rows(const Plan& p, int64_t row_bytes) {
+  const int64_t bytes = p.R <= kSmallRows ? 64000000 : 48000000 * p.passes;
+  return std::min(p.Vt, bytes / row_bytes);
+}
+
+// CTAs that zero those rows: one per 16 KB of each of `parts` kernels, up to `most`.
+inline int fill_ctas(const Plan& p, int64_t row_bytes, int parts, int most) {
+  return int(std::min<int64_t>(most, (p.fill * row_bytes / parts + 16383) / 16384));
 }
 
 struct View {

@@ -150,7 +150,7 @@ dspark_status_t dspark_embed_bwd(const dspark_embed_problem_t* prob, const void*
   a.table_f32 = dtable_dtype == DSPARK_F32;
   a.accumulate = accumulate ? 1 : 0;
   a.plan = embed_plan(prob);
-  if (!accumulate) embed::plan_fill(a.plan, prob->D * elem_size(dtable_dtype));
+  if (!accumulate) a.plan.fill = embed::fill_rows(a.plan, prob->D * elem_size(dtable_dtype));
   a.ws = embed::view(ws, a.plan);
   return cuda_status(embed::launch_bwd(a, reinterpret_cast<cudaStream_t>(stream)));
 }
