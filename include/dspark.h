@@ -366,6 +366,10 @@ typedef struct {
   int64_t ignore_index;        /* e.g. -100; wins where it lies in [0, V)               */
   const float* row_weight;     /* [R] w_r, or NULL = 1                                  */
   float z_alpha;               /* weight of lse^2; 0 = plain cross entropy              */
+  int64_t hidden_grad_only;    /* 1: the backward will be asked for dhidden alone (a
+                                  frozen head).  At large vocabularies the forward then
+                                  gathers it as it goes, which saves one of three products;
+                                  its workspace is the backward's.                      */
 } dspark_lce_problem_t;
 
 /* Forward outputs; each may be NULL. */
@@ -376,7 +380,8 @@ typedef struct {
   float* lse_rows;             /* [R] logsumexp per row, 0 without a label              */
 } dspark_lce_out_t;
 
-/* Gradients; dhidden and dweight may each be NULL (a frozen head, a frozen drafter). */
+/* Gradients; dhidden and dweight may each be NULL (a frozen head, a frozen drafter).  They
+ * overlap neither each other nor the inputs. */
 typedef struct {
   const float* grad_scale;     /* device scalar g = d(objective)/d(loss_num); NULL = 1  */
   void* dhidden;               /* bf16 [R, H], written for every row                    */
@@ -400,7 +405,8 @@ DSPARK_API dspark_status_t dspark_lce_fwd(const dspark_lce_problem_t* prob, cons
 
 /* Backward of the dspark_lce_fwd that last ran on `ws`, with the same problem: reads the
  * row list, the labelled hidden rows and the logsumexps it left there, and weight again.
- * May be called more than once after one forward. */
+ * May be called more than once after one forward.  dweight with hidden_grad_only is
+ * DSPARK_ERR_INVALID_ARG. */
 DSPARK_API dspark_status_t dspark_lce_bwd(const dspark_lce_problem_t* prob, const dspark_lce_grads_t* grads, void* ws,
                                           size_t ws_bytes, dspark_stream_t stream);
 

@@ -12,7 +12,8 @@ import torch
 def linear_ce(hidden, weight, targets, row_weight=None, ignore_index=-100, z_alpha=0.0, grad_scale=1.0):
     """Loss, row outputs and gradients, and the magnitudes the error bounds need:
     ``reach`` = max over labelled rows and the vocabulary of sum_k |h_k w_k|, ``dh_mag`` and
-    ``dw_mag`` = |dz| |weight| and |dz|^T |hidden|."""
+    ``dw_mag`` = |dz| |weight| and |dz|^T |hidden|, ``dh_pmag`` and ``dw_pmag`` the same with
+    the probabilities' part of dz alone."""
     V = weight.shape[0]
     live = (targets != ignore_index) & (targets >= 0) & (targets < V)
     h = torch.where(live[:, None], hidden, torch.zeros_like(hidden)).double()
@@ -23,12 +24,14 @@ def linear_ce(hidden, weight, targets, row_weight=None, ignore_index=-100, z_alp
     lse = torch.logsumexp(z, dim=1)
     ce = lse - z.gather(1, t[:, None])[:, 0]
     dz = torch.exp(z - lse[:, None]) * (1.0 + 2.0 * z_alpha * lse)[:, None]
+    dp = dz * (grad_scale * a)[:, None].abs()
     dz.scatter_add_(1, t[:, None], torch.full_like(dz[:, :1], -1.0))
     dz *= (grad_scale * a)[:, None]
     zero = torch.zeros_like(lse)
     return dict(loss_num=(a * (ce + z_alpha * lse * lse)).sum(), num_tokens=int(live.sum()),
                 ce_rows=torch.where(live, ce, zero), lse_rows=torch.where(live, lse, zero),
                 dhidden=dz @ w, dweight=dz.T @ h, dh_mag=dz.abs() @ w.abs(), dw_mag=dz.abs().T @ h.abs(),
+                dh_pmag=dp.abs() @ w.abs(), dw_pmag=dp.abs().T @ h.abs(),
                 reach=float((h.abs() @ w.abs().T).max()) if bool(live.any()) else 0.0)
 
 

@@ -95,7 +95,7 @@ class dspark_lce_problem_t(ctypes.Structure):
         ("hidden", c_vp), ("hidden_ld", c_i64),
         ("weight", c_vp), ("weight_ld", c_i64),
         ("targets", c_vp), ("ignore_index", c_i64),
-        ("row_weight", c_vp), ("z_alpha", ctypes.c_float),
+        ("row_weight", c_vp), ("z_alpha", ctypes.c_float), ("hidden_grad_only", c_i64),
     ]
 
 

@@ -1,6 +1,6 @@
 // Linear cross entropy: softmax cross entropy of z = hidden . weight^T over the whole
 // vocabulary and its gradients, the logits never kept.
-//   forward   prep:  the labelled rows' list, their hidden rows gathered compact
+//   forward   prep:  the labelled rows' places, their hidden rows gathered compact
 //             fwd:   product tiles; each row's (maximum, sum of exponentials) in the tile
 //             merge: logsumexp, CE and the loss from the tiles' pairs
 //   backward, a piece of the vocabulary at a time:
@@ -8,6 +8,10 @@
 //             dw:    dweight rows of the piece = dz^T . hidden
 //             dh:    partial sums of dhidden = dz . weight, FP32
 //             then dhidden from the partial sums, scattered to the labelled rows
+//   Where no head gradient follows (hidden_grad_only), the forward gathers the hidden
+//   gradient as it goes, like attention's softmax: sum_v exp(z_v - ref) weight_v beside
+//   sum_v exp(z_v - ref), with one product less (1600 labelled rows of 4096 against 151936
+//   columns: 4510 us without, 3226 us with it).
 // A label's row appears in no product unless it is labelled (ignore_index rows are neither
 // read nor computed), so masked batches pay for their labels only.
 //
@@ -37,7 +41,7 @@ constexpr int kThreads = 64 + 32 * kEpiWarps;
 
 // ------------------------------------------------------------------ prep
 // Each CTA takes a contiguous run of rows, counts the labelled rows before it (the labels
-// are small and in L2) and writes its part of the list; then it copies its labelled hidden
+// are small and in L2) and writes its rows' places; then it copies its labelled hidden
 // rows.  The last CTA, which sees every row, writes the counts and the status and
 // zero-fills the compact rows up to a whole 64-row K chunk: the dweight product reads
 // those, and zero is what they have to add.
@@ -94,7 +98,6 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const dspark_lce_pro
     }
     if (r < r1) ws.index[r] = live ? at : -1;
     if (live) {
-      ws.list[at] = int32_t(r);
       ws.tok[at] = int32_t(t);
       ws.w[at] = p.row_weight ? p.row_weight[r] : 1.f;
     }
@@ -133,6 +136,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const dspark_lce_pro
       ws.hdr->status = sh_bad ? kFlagIdOutOfRange : 0u;
       ws.hdr->n_valid = base;
       ws.hdr->done = 0;
+      ws.hdr->redo = 0;
       if (num_tokens) *num_tokens = base;
     }
   }
@@ -177,7 +181,7 @@ __device__ __forceinline__ Item decode(const Work& wk, int w, int me, int kch, i
   return it;
 }
 
-enum : int { kFwd = 0, kDz = 1, kDh = 2, kDwBf16 = 3, kDwF32 = 4 };
+enum : int { kFwd = 0, kDz = 1, kDh = 2, kDwBf16 = 3, kDwF32 = 4, kGather = 5 };
 
 struct EpiArgs {
   View ws;
@@ -187,6 +191,7 @@ struct EpiArgs {
   float z_alpha;
   const float* grad_scale;
   int32_t add;               // dh: add to the planes; dw: add to dweight
+  int32_t if_redo;           // only where a gathered forward has to be done the other way
 };
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
@@ -383,6 +388,58 @@ __device__ __forceinline__ void dz_finish(const EpiArgs& a, const CUtensorMap& o
   }
 }
 
+// Gathered forward: the row's exponentials relative to its reference, as bf16 for the product
+// with the head and summed in FP32; the logit at the label.  The label's column is left out
+// of the product: its factor in the gradient is p - 1, which for a row that is nearly right
+// is far below the rounding of p.  A logit 100 octaves above the
+// reference (69 above the largest of the sampled columns) would leave bf16's and FP32's range
+// in the sums: it is reported, and the call goes the other way.
+__device__ __forceinline__ void gather_finish(const EpiArgs& a, const CUtensorMap& out, Share& sh, float (&z)[128]) {
+  if (sh.m0 >= a.rows) return;  // the whole warp
+  const int row = sh.m0 + sh.lane;
+  const bool live = row < sh.n_valid;
+  const int n0 = sh.n0 + sh.c0;
+  const int tgt = live ? a.ws.tok[row] - a.col0 - n0 : -1;
+  const float ref = live ? a.ws.ref[row] : 0.f;
+  const int cols = live ? a.n_cols - n0 : 0;
+  float s4[4] = {0.f, 0.f, 0.f, 0.f}, top = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 128; c += 64) {
+    uint32_t o[32];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int cc = c + 32 * h;
+      float* v = z + cc;
+      const int at = tgt < cols ? tgt - cc : -1;
+      if (uint32_t(at) < 32u) {
+        float zt = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) zt = at == i ? v[i] : zt;
+        a.ws.zt[row] = zt;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float x = fmaf(v[i], kLog2e, -ref);
+        const bool in = cols - cc >= 32 || i < cols - cc;
+        top = in ? fmaxf(top, x) : top;
+        v[i] = in ? ex2(x) : 0.f;
+        s4[i & 3] += v[i];
+      }
+      if (uint32_t(at) < 32u) {  // the label's own term is not rounded: it is added at the end
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = at == i ? 0.f : v[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[16 * h + i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    }
+    store_box(sh, out, o, n0 + c, sh.m0, 0, staging_tiles(kGather));
+  }
+  if (!live) return;
+  if (top > 100.f) a.ws.hdr->redo = 1;  // every writer writes the same
+  a.ws.part[size_t(2 * (a.col0 / kBN + sh.nt) + sh.half) * a.plan.Rp + row] =
+      make_float2(ref, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+}
+
 // FP32 results: dhidden's partial sums (one plane per K split; a plane's element gets one
 // addition per piece, in stream order, so the sums have a fixed order), or dweight.
 template <int EPI>
@@ -418,13 +475,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmO, const Work wk, const EpiArgs ea, const int bn) {
   constexpr bool A_MN = EPI == kDwBf16 || EPI == kDwF32;
-  constexpr bool B_MN = EPI != kFwd && EPI != kDz;
+  constexpr bool B_MN = EPI != kFwd && EPI != kDz && EPI != kGather;
   constexpr int STAGES = stages<CG>(EPI);
   // The tensor cores' FP32 accumulation rounds towards zero: over K = 4096 the logits come
   // out 2.2e-6 short (relative), over K = 512 3e-7.  The forward hands over its accumulator
   // every 512 values of K and the epilogue adds the segments in registers, rounding to
   // nearest; the other products are rounded to bf16 right after, where it does not show.
-  constexpr int SEG = EPI == kFwd ? 512 / BK : 1 << 29;
+  constexpr int SEG = EPI == kFwd || EPI == kGather ? 512 / BK : 1 << 29;
   constexpr uint32_t SA = kBM * BK * 2, SS = stage_bytes<CG>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -481,7 +538,8 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const int me = wk.bound_m ? min(wk.m_tiles, (n_valid + kBM * CG - 1) / (kBM * CG)) : wk.m_tiles;
   const int kch = wk.bound_k ? min(wk.kchunks, (n_valid + BK - 1) / BK) : wk.kchunks;
   const int ks = EPI == kDh ? splits_of(ea.plan, me) : 1;
-  const int W = me * wk.n_tiles * ks;  // the same in every role
+  const bool off = ea.if_redo && ea.ws.hdr->redo == 0;
+  const int W = off ? 0 : me * wk.n_tiles * ks;  // the same in every role
   bool timed_out = false;
 
   if (warp == 0 && lane == 0) {
@@ -573,7 +631,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const Item t = decode(wk, w, me, kch, ks);
       sh.m0 = (t.mt * CG + int(rank)) * kBM + q * 32, sh.n0 = t.nt * bn;
       sh.nt = t.nt, sh.plane0 = t.s * me * kBM * CG, sh.empty = t.kc0 == t.kc1;
-      if constexpr (EPI == kFwd) {
+      if constexpr (EPI == kFwd || EPI == kGather) {
         float z[128];
 #pragma unroll
           for (int i = 0; i < 128; ++i) z[i] = 0.f;
@@ -593,7 +651,8 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           }
           release(b);
         }
-        fwd_finish(ea, sh, z);
+        if constexpr (EPI == kFwd) fwd_finish(ea, sh, z);
+        else gather_finish(ea, tmO, sh, z);
       } else {
         const int b = tl & 1;
         if (!mbar_wait_bounded(accf0 + 8 * b, uint32_t(tl >> 1) & 1u)) timed_out = true;
@@ -629,9 +688,10 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 constexpr int kSlices = 32;
 
 __global__ void __launch_bounds__(kSlices * 32) merge_kernel(const View ws, const Plan pl, const float z_alpha,
-                                                             const dspark_lce_out_t out) {
+                                                             const dspark_lce_out_t out, const int if_redo) {
   pdl_wait();
   pdl_trigger();
+  if (if_redo && ws.hdr->redo == 0) return;
   __shared__ float2 sp[kSlices][kMergeRows];
   __shared__ double sd[32];
   __shared__ int is_last;
@@ -701,7 +761,9 @@ __global__ void __launch_bounds__(kSlices * 32) merge_kernel(const View ws, cons
     }
   }
   __syncthreads();
-  if (!is_last || out.loss_num == nullptr) return;
+  if (!is_last) return;
+  if (threadIdx.x == 0) ws.hdr->done = 0;  // for a second merge of the call
+  if (out.loss_num == nullptr) return;
   __threadfence();
   double acc = 0.0;
   for (int64_t k = threadIdx.x; k < gridDim.x; k += blockDim.x) acc += __ldcg(ws.loss_part + k);
@@ -716,14 +778,34 @@ __global__ void __launch_bounds__(kSlices * 32) merge_kernel(const View ws, cons
   }
 }
 
+// ------------------------------------------------------------------ reference
+// A gathered row's reference: the largest logit of the sampled columns (one that is not a
+// number, or infinite, is left to the exponentials to show).
+__global__ void __launch_bounds__(256) reference_kernel(const View ws, const Plan pl) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= ws.hdr->n_valid) return;
+  float m = -INFINITY;
+#pragma unroll
+  for (int t = 0; t < 2 * kSampleCols / kBN; ++t) m = fmaxf(m, ws.part[size_t(t) * pl.Rp + i].x);
+  ws.ref[i] = fabsf(m) < INFINITY ? m : 0.f;
+}
+
 // ------------------------------------------------------------------ dhidden
-// The planes' sums in plane order, rounded once; rows without a label are zero.
-__global__ void __launch_bounds__(256) dhidden_kernel(const View ws, const Plan pl, uint16_t* dh, int64_t ld) {
+// The planes' sums in plane order, rounded once; rows without a label are zero.  After a
+// gathered forward the planes hold the sum over v != target of 2^(z log2 e - ref) weight_v,
+// and here, with c = 1 + 2 z_alpha lse,
+//   dhidden_r = g w (c 2^(ref - lse2) that + (c 2^(z_target log2 e - lse2) - 1) weight[target])
+__global__ void __launch_bounds__(256) dhidden_kernel(const View ws, const Plan pl, const dspark_lce_problem_t p,
+                                                      const float* grad_scale, uint16_t* dh, int64_t ld) {
   pdl_wait();
   pdl_trigger();
   const int64_t h8 = pl.H / 8, n = pl.R * h8;
   const int tile = kBM * pl.cg, me = (ws.hdr->n_valid + tile - 1) / tile, splits = splits_of(pl, me);
   const size_t plane = size_t(me) * tile * pl.H;
+  const bool gathered = pl.gathered && ws.hdr->redo == 0;
+  const float g = pl.gathered && grad_scale ? *grad_scale : 1.f;  // else dz has it
   for (int64_t k = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; k < n; k += int64_t(gridDim.x) * blockDim.x) {
     const int64_t r = k / h8, j = (k - r * h8) * 8;
     const int i = ws.index[r];
@@ -736,6 +818,20 @@ __global__ void __launch_bounds__(256) dhidden_kernel(const View ws, const Plan 
         const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 4);
         a[0] += x.x, a[1] += x.y, a[2] += x.z, a[3] += x.w;
         a[4] += y.x, a[5] += y.y, a[6] += y.z, a[7] += y.w;
+      }
+      if (gathered) {
+        const float lse2 = ws.lse2[i], gw = g * ws.w[i];
+        const float c = gw * fmaf(2.f * p.z_alpha, lse2 * kLn2, 1.f);
+        const float f = c * ex2(ws.ref[i] - lse2), ft = ex2(fmaf(ws.zt[i], kLog2e, -lse2)) * c - gw;
+        const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.weight) +
+                                                        size_t(ws.tok[i]) * p.weight_ld + j);
+        const float t[8] = {bf16lo(q.x), bf16hi(q.x), bf16lo(q.y), bf16hi(q.y),
+                            bf16lo(q.z), bf16hi(q.z), bf16lo(q.w), bf16hi(q.w)};
+#pragma unroll
+        for (int u = 0; u < 8; ++u) a[u] = fmaf(f, a[u], ft * t[u]);
+      } else if (pl.gathered) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) a[u] *= g;
       }
       o = make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
     }
@@ -778,33 +874,39 @@ Work make_work(int m_tiles, int n_tiles, int kchunks, int group, bool over_rows,
               inverse(uint32_t(group) * uint32_t(n_tiles)), inverse(uint32_t(group))};
 }
 
-}  // namespace
+cudaError_t launch_merge(const dspark_lce_problem_t& p, const dspark_lce_out_t& out, const Plan& pl, const View& ws,
+                         bool if_redo, cudaStream_t s) {
+  PdlLaunch l(pl.merge_blocks, kSlices * 32, 0, s);
+  return cudaLaunchKernelEx(&l.cfg, merge_kernel, ws, pl, p.z_alpha, out, int(if_redo));
+}
 
-cudaError_t launch_fwd(const dspark_lce_problem_t& p, const dspark_lce_out_t& out, const Plan& pl, const View& ws,
-                       cudaStream_t s) {
-  const int64_t ctas = std::min<int64_t>(p.R, 4 * kSlots);
-  const int64_t rows_per_cta = ceil_div(p.R, ctas);
-  PdlLaunch first(ceil_div(p.R, rows_per_cta), kPrepThreads, 0, s);
-  first.cfg.numAttrs = 0;  // the first kernel of the call waits for all work before it
-  cudaError_t e = cudaLaunchKernelEx(&first.cfg, prep_kernel, p, ws, out.num_tokens, rows_per_cta);
-  if (e != cudaSuccess) return e;
+// The forward product over the first `cols` columns, then the rows' logsumexps (all columns)
+// or references (a sample of them).
+cudaError_t launch_logsumexp(const dspark_lce_problem_t& p, const dspark_lce_out_t& out, const Plan& pl, const View& ws,
+                             int64_t cols, bool if_redo, cudaStream_t s) {
   CUtensorMap ma, mb;
   if (!tc::make_map(&ma, ws.hsup, pl.Rp, p.H, p.H, 64, kBM) ||
       !tc::make_map(&mb, p.weight, p.V, p.H, p.weight_ld, 64, kBN / pl.cg))
     return cudaErrorInvalidValue;
-  const Work wk = make_work(tiles(p.R, kBM * pl.cg), tiles(p.V, kBN), tiles(p.H, BK), 16, false, ws);
+  const Work wk = make_work(tiles(p.R, kBM * pl.cg), tiles(cols, kBN), tiles(p.H, BK), 16, false, ws);
   EpiArgs ea{};
   ea.ws = ws;
   ea.plan = pl;
   ea.rows = int32_t(pl.Rp);
-  ea.n_cols = int32_t(p.V);
-  if ((e = product<kFwd>(pl, ma, mb, ma, wk, ea, kBN, s)) != cudaSuccess) return e;
-  PdlLaunch l(pl.merge_blocks, kSlices * 32, 0, s);
-  return cudaLaunchKernelEx(&l.cfg, merge_kernel, ws, pl, p.z_alpha, out);
+  ea.n_cols = int32_t(cols);
+  ea.if_redo = if_redo;
+  const cudaError_t e = product<kFwd>(pl, ma, mb, ma, wk, ea, kBN, s);
+  if (e != cudaSuccess) return e;
+  if (cols == p.V) return launch_merge(p, out, pl, ws, if_redo, s);
+  PdlLaunch l(ceil_div(p.R, 256), 256, 0, s);
+  return cudaLaunchKernelEx(&l.cfg, reference_kernel, ws, pl);
 }
 
-cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& g, const Plan& pl, const View& ws,
-                       cudaStream_t s) {
+// A piece of the vocabulary at a time: dL/dz (kDz) or a gathered forward's exponentials
+// (kGather) into the workspace, and the products with them.  In a gathered call kDz is the
+// other way, taken only where a row asked for it.
+cudaError_t launch_pieces(const dspark_lce_problem_t& p, const dspark_lce_grads_t& g, const Plan& pl, const View& ws,
+                          int what, bool dhidden, cudaStream_t s) {
   const bool f32 = g.dweight_dtype == DSPARK_F32;
   cudaError_t e;
   CUtensorMap h_k, h_mn;
@@ -826,8 +928,11 @@ cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& 
     ea.col0 = int32_t(v0);
     ea.z_alpha = p.z_alpha;
     ea.grad_scale = g.grad_scale;
+    ea.if_redo = pl.gathered && what == kDz;
     const Work wz = make_work(tiles(p.R, kBM * pl.cg), tiles(n, kBN), tiles(p.H, BK), 16, false, ws);
-    if ((e = product<kDz>(pl, h_k, w_k, z_out, wz, ea, kBN, s)) != cudaSuccess) return e;
+    e = what == kGather ? product<kGather>(pl, h_k, w_k, z_out, wz, ea, kBN, s)
+                        : product<kDz>(pl, h_k, w_k, z_out, wz, ea, kBN, s);
+    if (e != cudaSuccess) return e;
     if (g.dweight) {
       void* d0 = static_cast<uint8_t*>(g.dweight) + size_t(v0) * g.dweight_ld * (f32 ? 4 : 2);
       if (!tc::make_map(&z_mn, ws.dz, pl.Rp, ldz, ldz, 64, 64) ||
@@ -841,7 +946,7 @@ cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& 
               : product<kDwBf16>(pl, z_mn, h_mn, o, ww, ea, pl.bn_h, s);
       if (e != cudaSuccess) return e;
     }
-    if (g.dhidden) {
+    if (dhidden) {
       if (!tc::make_map(&w_mn, w0, n, p.H, p.weight_ld, 64, 64) || !tc::make_map(&z_k, ws.dz, pl.Rp, ldz, ldz, 64, kBM) ||
           !tc::make_out_map(&o, ws.planes, pl.plane_rows, p.H, p.H))
         return cudaErrorInvalidValue;
@@ -854,12 +959,40 @@ cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& 
       if ((e = product<kDh>(pl, z_k, w_mn, o, wh, ea, pl.bn_h, s)) != cudaSuccess) return e;
     }
   }
-  if (g.dhidden) {
-    const int64_t blocks = std::min<int64_t>(ceil_div(p.R * (p.H / 8), 256), 8 * kSlots);
-    PdlLaunch l(blocks, 256, 0, s);
-    return cudaLaunchKernelEx(&l.cfg, dhidden_kernel, ws, pl, static_cast<uint16_t*>(g.dhidden), g.dhidden_ld);
-  }
   return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_fwd(const dspark_lce_problem_t& p, const dspark_lce_out_t& out, const Plan& pl, const View& ws,
+                       cudaStream_t s) {
+  const int64_t ctas = std::min<int64_t>(p.R, 4 * kSlots);
+  const int64_t rows_per_cta = ceil_div(p.R, ctas);
+  PdlLaunch first(ceil_div(p.R, rows_per_cta), kPrepThreads, 0, s);
+  first.cfg.numAttrs = 0;  // the first kernel of the call waits for all work before it
+  cudaError_t e = cudaLaunchKernelEx(&first.cfg, prep_kernel, p, ws, out.num_tokens, rows_per_cta);
+  if (e != cudaSuccess) return e;
+  if (!pl.gathered) return launch_logsumexp(p, out, pl, ws, p.V, false, s);
+  // the reference from a few columns, then the logsumexp and the hidden gradient in one pass
+  if ((e = launch_logsumexp(p, out, pl, ws, kSampleCols, false, s)) != cudaSuccess) return e;
+  dspark_lce_grads_t none{};
+  if ((e = launch_pieces(p, none, pl, ws, kGather, true, s)) != cudaSuccess) return e;
+  if ((e = launch_merge(p, out, pl, ws, false, s)) != cudaSuccess) return e;
+  // and where a row left the range of its reference, both again from its own maximum
+  if ((e = launch_logsumexp(p, out, pl, ws, p.V, true, s)) != cudaSuccess) return e;
+  return launch_pieces(p, none, pl, ws, kDz, true, s);
+}
+
+cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& g, const Plan& pl, const View& ws,
+                       cudaStream_t s) {
+  cudaError_t e;
+  if (!pl.gathered && (e = launch_pieces(p, g, pl, ws, kDz, g.dhidden != nullptr, s)) != cudaSuccess) return e;
+  if (!g.dhidden) return cudaSuccess;
+  const int64_t blocks = std::min<int64_t>(ceil_div(p.R * (p.H / 8), 256), 8 * kSlots);
+  PdlLaunch l(blocks, 256, 0, s);
+  if (pl.gathered) l.cfg.numAttrs = 0;  // the first kernel of the call
+  return cudaLaunchKernelEx(&l.cfg, dhidden_kernel, ws, pl, p, g.grad_scale, static_cast<uint16_t*>(g.dhidden),
+                            g.dhidden_ld);
 }
 
 }  // namespace lce

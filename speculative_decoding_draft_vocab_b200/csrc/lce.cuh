@@ -15,13 +15,18 @@ constexpr size_t kPieceBytes = size_t(256) << 20;    // bound on the kept piece 
 constexpr int kMaxSplitTiles = 32;                   // more row tiles than this are not split
 constexpr int kMaxSplit = 32;
 constexpr size_t kPlaneBytes = size_t(96) << 20;     // bound on split planes (they stay in L2)
+// A gathered forward takes the reference of a row's exponentials from this many columns.
+constexpr int kSampleCols = 2048;
+// From this vocabulary on it pays: it saves one of three products and adds the sample.
+constexpr int64_t kGatherFrom = 16384;
 constexpr int kMergeRows = 32;                       // rows per CTA of the merge kernel
 
 struct WsLceHeader {
   uint32_t status;     // device error bits
   int32_t n_valid;     // labelled rows
   uint32_t done;       // merge CTAs finished
-  uint32_t pad[61];
+  uint32_t redo;       // gathered forward: a row's exponentials left their range
+  uint32_t pad[60];
 };
 static_assert(sizeof(WsLceHeader) == 256, "header is one 256-byte line");
 
@@ -37,17 +42,18 @@ struct Plan {
   int64_t plane_rows;  // rows of the hidden gradient's partial sums, all planes together
   uint8_t ksplit[kMaxSplitTiles + 1];  // its K splits (planes) by the number of row tiles
   int64_t merge_blocks;
+  int gathered;        // the forward also gathers the hidden gradient (no head gradient follows)
 };
 
 struct View {
   WsLceHeader* hdr;
   double* loss_part;   // [merge_blocks]
-  int32_t* list;       // [R] labelled rows in row order
-  int32_t* index;      // [R] position of a row in `list`, -1 without a label
+  int32_t* index;      // [R] position of a row among the labelled ones, -1 without a label
   int32_t* tok;        // [R] label of the i-th labelled row
   float* w;            // [R] weight of the i-th labelled row
   float* lse2;         // [R] base-2 logsumexp of the i-th labelled row
   float* zt;           // [R] logit at the label
+  float* ref;          // [R] base-2 exponent that a gathered row's exponentials are relative to
   uint16_t* hsup;      // [Rp][H] bf16 labelled hidden rows, compact, zeros up to a whole chunk
   float2* part;        // [2 fwd_tiles][Rp] (base-2 maximum, sum) of a row's columns in half a tile
   uint16_t* dz;        // [Rp][piece] bf16 piece of dL/dlogits
@@ -56,7 +62,7 @@ struct View {
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-inline Plan make_plan(int64_t R, int64_t V, int64_t H) {
+inline Plan make_plan(int64_t R, int64_t V, int64_t H, bool hidden_grad_only) {
   Plan p{};
   p.R = R, p.V = V, p.H = H;
   p.Rp = ceil_div(R, 64) * 64;
@@ -73,7 +79,7 @@ inline Plan make_plan(int64_t R, int64_t V, int64_t H) {
   // hold the labelled rows), so there is a number of splits for each count.
   const int64_t n_tiles = ceil_div(H, p.bn_h), chunks = ceil_div(std::min(V, p.piece), 64);
   p.plane_rows = R;
-  for (int64_t m = 1; m <= kMaxSplitTiles; ++m) {
+  for (int64_t m = 1; m <= std::min<int64_t>(kMaxSplitTiles, m_tiles); ++m) {
     int best = 1;
     int64_t cost = INT64_MAX;
     for (int k = 1; k <= kMaxSplit && (k == 1 || chunks / k >= 8); ++k) {
@@ -82,9 +88,10 @@ inline Plan make_plan(int64_t R, int64_t V, int64_t H) {
       if (c < cost) cost = c, best = k;
     }
     p.ksplit[m] = uint8_t(best);
-    if (m <= m_tiles && best > 1) p.plane_rows = std::max(p.plane_rows, m * best * kBM * p.cg);
+    if (best > 1) p.plane_rows = std::max(p.plane_rows, m * best * kBM * p.cg);
   }
   p.merge_blocks = ceil_div(R, kMergeRows);
+  p.gathered = hidden_grad_only && V >= kGatherFrom;
   return p;
 }
 
@@ -94,25 +101,25 @@ __host__ __device__ inline int splits_of(const Plan& p, int row_tiles) {
 }
 
 struct Offsets {
-  size_t hdr, loss_part, list, index, tok, w, lse2, zt, hsup, part, fwd_bytes, dz, planes, bytes;
+  size_t hdr, loss_part, index, tok, w, lse2, zt, ref, hsup, part, dz, planes, bytes;
 };
 
 inline Offsets offsets(const Plan& p, bool bwd, bool dhidden) {
+  if (p.gathered) bwd = dhidden = true;
   Offsets o{};
   size_t off = 0;
   const size_t R = size_t(p.R), Rp = size_t(p.Rp);
   auto take = [&](size_t& at, size_t n) { at = off; off = align256(off + n); };
   take(o.hdr, sizeof(WsLceHeader));
   take(o.loss_part, sizeof(double) * size_t(p.merge_blocks));
-  take(o.list, 4 * R);
   take(o.index, 4 * R);
   take(o.tok, 4 * R);
   take(o.w, 4 * R);
   take(o.lse2, 4 * R);
   take(o.zt, 4 * R);
+  take(o.ref, 4 * R);
   take(o.hsup, 2 * Rp * size_t(p.H));
   take(o.part, sizeof(float2) * 2 * size_t(p.fwd_tiles) * Rp);
-  o.fwd_bytes = off;
   take(o.dz, bwd ? 2 * Rp * size_t(p.piece) : 0);
   take(o.planes, bwd && dhidden ? sizeof(float) * size_t(p.plane_rows) * size_t(p.H) : 0);
   o.bytes = off;
@@ -125,12 +132,12 @@ inline View view(void* base, const Plan& p) {
   View v{};
   v.hdr = reinterpret_cast<WsLceHeader*>(b + o.hdr);
   v.loss_part = reinterpret_cast<double*>(b + o.loss_part);
-  v.list = reinterpret_cast<int32_t*>(b + o.list);
   v.index = reinterpret_cast<int32_t*>(b + o.index);
   v.tok = reinterpret_cast<int32_t*>(b + o.tok);
   v.w = reinterpret_cast<float*>(b + o.w);
   v.lse2 = reinterpret_cast<float*>(b + o.lse2);
   v.zt = reinterpret_cast<float*>(b + o.zt);
+  v.ref = reinterpret_cast<float*>(b + o.ref);
   v.hsup = reinterpret_cast<uint16_t*>(b + o.hsup);
   v.part = reinterpret_cast<float2*>(b + o.part);
   v.dz = reinterpret_cast<uint16_t*>(b + o.dz);

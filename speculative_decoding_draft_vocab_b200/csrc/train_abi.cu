@@ -23,11 +23,13 @@ dspark_status_t check_lce_call(const dspark_lce_problem_t* p) {
   if (st != DSPARK_OK) return st;
   if (!p->hidden || !p->weight || !p->targets) return DSPARK_ERR_INVALID_ARG;
   if (p->hidden_ld < p->H || p->weight_ld < p->H) return DSPARK_ERR_INVALID_ARG;
-  if (!(p->z_alpha >= 0.f)) return DSPARK_ERR_INVALID_ARG;
+  if (!(p->z_alpha >= 0.f) || (p->hidden_grad_only != 0 && p->hidden_grad_only != 1)) return DSPARK_ERR_INVALID_ARG;
   if (p->H % 8 || p->hidden_ld % 8 || p->weight_ld % 8 || !aligned16(p->hidden) || !aligned16(p->weight))
     return DSPARK_ERR_ALIGNMENT;
   return DSPARK_OK;
 }
+
+lce::Plan lce_plan(const dspark_lce_problem_t* p) { return lce::make_plan(p->R, p->V, p->H, p->hidden_grad_only != 0); }
 
 dspark_status_t check_ws(const void* ws, size_t have, size_t need) {
   if (ws == nullptr) return DSPARK_ERR_WORKSPACE;
@@ -82,7 +84,7 @@ extern "C" {
 size_t dspark_lce_workspace_size(const dspark_lce_problem_t* prob, const dspark_lce_grads_t* grads) {
   if (check_lce(prob) != DSPARK_OK) return 0;
   const bool bwd = grads && (grads->dhidden || grads->dweight);
-  return lce::offsets(lce::make_plan(prob->R, prob->V, prob->H), bwd, bwd && grads->dhidden).bytes;
+  return lce::offsets(lce_plan(prob), bwd, bwd && grads->dhidden).bytes;
 }
 
 dspark_status_t dspark_lce_fwd(const dspark_lce_problem_t* prob, const dspark_lce_out_t* out, void* ws,
@@ -91,7 +93,7 @@ dspark_status_t dspark_lce_fwd(const dspark_lce_problem_t* prob, const dspark_lc
   dspark_status_t st = check_lce_call(prob);
   if (st != DSPARK_OK) return st;
   if ((st = check_ws(ws, ws_bytes, dspark_lce_workspace_size(prob, nullptr))) != DSPARK_OK) return st;
-  const lce::Plan plan = lce::make_plan(prob->R, prob->V, prob->H);
+  const lce::Plan plan = lce_plan(prob);
   return cuda_status(lce::launch_fwd(*prob, *out, plan, lce::view(ws, plan), reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -105,6 +107,7 @@ dspark_status_t dspark_lce_bwd(const dspark_lce_problem_t* prob, const dspark_lc
     if (!aligned16(grads->dhidden) || grads->dhidden_ld % 8) return DSPARK_ERR_ALIGNMENT;
   }
   if (grads->dweight) {
+    if (prob->hidden_grad_only) return DSPARK_ERR_INVALID_ARG;
     const bool f32 = grads->dweight_dtype == DSPARK_F32;
     if (!f32 && grads->dweight_dtype != DSPARK_BF16) return DSPARK_ERR_INVALID_ARG;
     if (grads->dweight_ld < prob->H) return DSPARK_ERR_INVALID_ARG;
@@ -112,7 +115,7 @@ dspark_status_t dspark_lce_bwd(const dspark_lce_problem_t* prob, const dspark_lc
     if (!aligned16(grads->dweight) || grads->dweight_ld % (f32 ? 4 : 8)) return DSPARK_ERR_ALIGNMENT;
   }
   if ((st = check_ws(ws, ws_bytes, dspark_lce_workspace_size(prob, grads))) != DSPARK_OK) return st;
-  const lce::Plan plan = lce::make_plan(prob->R, prob->V, prob->H);
+  const lce::Plan plan = lce_plan(prob);
   return cuda_status(lce::launch_bwd(*prob, *grads, plan, lce::view(ws, plan), reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -460,7 +460,9 @@ class LinearCE(_DeviceCall):
     int64, ``row_weight`` [R] fp32.  forward() writes ``loss_num``, ``num_tokens``,
     ``ce_rows``, ``lse_rows``; backward() writes ``dhidden`` (bf16) and ``dweight``
     (``dweight_dtype``; with ``accumulate`` added to, fp32 only).  Pass tensors for
-    ``dhidden`` / ``dweight`` to have them written there, False to leave them out.
+    ``dhidden`` / ``dweight`` to have them written there (not overlapping the inputs), False
+    to leave them out; without dweight and at a large vocabulary the forward gathers dhidden
+    as it goes (hidden_grad_only of the C struct).
     ``grad_scale`` [1] fp32 may be filled before backward().
     """
 
@@ -497,6 +499,7 @@ class LinearCE(_DeviceCall):
             if dweight is True:
                 dweight = (torch.zeros if accumulate else torch.empty)(V, H, dtype=dweight_dtype, device=dev)
             self.dweight = dweight
+        p.hidden_grad_only = 1 if self.dhidden is not None and self.dweight is None else 0
         if self.dhidden is not None or self.dweight is not None:
             g = abi.dspark_lce_grads_t()
             g.grad_scale = _ptr(self.grad_scale)
@@ -519,16 +522,20 @@ class LinearCE(_DeviceCall):
         self.out = o
         grads = ctypes.byref(self.grads) if self.grads is not None else None
         self._workspace(int(abi.dspark_lce_workspace_size(ctypes.byref(p), grads)))
+        self._ran = False
         self._fwd_args = (ctypes.byref(p), ctypes.byref(o), self.ws_ptr, self.ws_len)
         self._bwd_args = (ctypes.byref(p), grads, self.ws_ptr, self.ws_len)
 
     def forward(self, stream=None) -> None:
         self._run(abi.dspark_lce_fwd, "dspark_lce_fwd", stream, *self._fwd_args)
+        self._ran = True
 
     def backward(self, stream=None) -> None:
         """The gradients of the last forward(), times ``grad_scale``."""
         if self.grads is None:
             raise ValueError("this call was built without gradients")
+        if not self._ran:
+            raise ValueError("backward() follows a forward()")
         self._run(abi.dspark_lce_bwd, "dspark_lce_bwd", stream, *self._bwd_args)
 
 

@@ -9,10 +9,12 @@ logits   The tensor cores add sixteen products at a time to an FP32 accumulator,
          2^-23 reach, reach = the largest sum_k |h_k w_k|.
 lse      within E, the 2^-21 of the exponentials, their sum and the logarithm, and the
          rounding of the value itself: E + 2^-20 + 2^-22 |lse|.  CE: E more.
-dz       relative: 2 E' + 2^-20 of the probabilities (E' = the unsegmented product's error,
-         (H / 16 + 2) 2^-23 reach, against lse's E), and u(bf16) of the rounding.
-dhidden  the relative error of dz times sum |dz w|, the accumulation ((n / 16 + 2) 2^-23 of the
-dweight  same, n the contracted length), and u of the result's own rounding.
+dz       p (relative) within P = 2 (E' + E) + 2^-20 (E' = the unsegmented product's error,
+         (H / 16 + 2) 2^-23 reach, against lse's E); dz = p - onehot is then off by P p, which
+         at the label of a nearly right row is more than P |dz|: p - 1 cancels what p's error
+         does not.  Rounding adds u(bf16) |dz|.
+dhidden  P sum |p w| + u(bf16) sum |dz w|, the accumulation ((n / 16 + 2) 2^-23 sum |dz w|, n
+dweight  the contracted length), and u of the result's own rounding.
 """
 
 import pytest
@@ -60,17 +62,17 @@ def lce_compare(call, ref, H, V, g=1.0, base=None):
     assert bool((lse[dead] == 0).all()) and bool((ce[dead] == 0).all())
     if call.grads is None:
         return
-    rel = 2 * ((H / 16 + 2) * 2.0 ** -23 * ref["reach"] + E) + 2.0 ** -20 + U16
+    P = 2 * ((H / 16 + 2) * 2.0 ** -23 * ref["reach"] + E) + 2.0 ** -20
     if call.dhidden is not None:
         want, mag = ref["dhidden"], ref["dh_mag"]
-        tol = (rel + (V / 16 + 2) * 2.0 ** -23) * mag + U16 * want.abs()
+        tol = P * ref["dh_pmag"] + (U16 + (V / 16 + 2) * 2.0 ** -23) * mag + U16 * want.abs()
         assert bool(((call.dhidden.double() - want).abs() <= tol * 1.01).all())
         none = call.dhidden[mag.sum(1) == 0]
         assert bool((none == 0).all())
     if call.dweight is not None:
         want, mag = ref["dweight"], ref["dw_mag"]
         got = call.dweight.double() - (0 if base is None else base.double())
-        tol = (rel + (R / 16 + 2) * 2.0 ** -23) * mag + _u(call.dweight.dtype) * want.abs()
+        tol = P * ref["dw_pmag"] + (U16 + (R / 16 + 2) * 2.0 ** -23) * mag + _u(call.dweight.dtype) * want.abs()
         if base is not None:
             tol = tol + U32 * (base.double().abs() + want.abs())
         assert bool(((got - want).abs() <= tol * 1.01).all())
@@ -138,6 +140,8 @@ def test_linear_ce_strides_scores_and_partial_gradients(T, R):
     assert torch.equal(score.ce_rows, both.ce_rows) and torch.equal(score.loss_num, both.loss_num)
     with pytest.raises(ValueError, match="without gradients"):
         score.backward()
+    with pytest.raises(ValueError, match="follows a forward"):
+        T.LinearCE(h, w, t).backward()
 
 
 @pytest.mark.parametrize("R", [50, 200])
@@ -248,6 +252,28 @@ def test_linear_ce_repeats_replays_and_keeps_to_its_stream(T, R, V):
     call.backward()
     assert all(torch.equal(x, y) for x, y in zip(replayed, snap()))
     lce_compare(call, O.linear_ce(h, w, t, a), H, V)
+
+
+def test_linear_ce_two_calls_at_once(T):
+    """Two calls with workspaces of their own, on two streams at the same time."""
+    made = []
+    for seed, (R, V, H) in enumerate([(300, 9000, 256), (90, 12000, 512)]):
+        h, w, t, a = lce_inputs(R, V, H, 9, seed=20 + seed)
+        alone = T.LinearCE(h, w, t, row_weight=a)
+        alone.forward()
+        alone.backward()
+        made.append((T.LinearCE(h, w, t, row_weight=a), alone, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for call, _, s in made:
+            with torch.cuda.stream(s):
+                call.forward()
+                call.backward()
+    torch.cuda.synchronize()
+    for call, alone, _ in made:
+        assert call.check_status() == 0
+        for k in ("loss_num", "ce_rows", "dhidden", "dweight"):
+            assert torch.equal(getattr(call, k), getattr(alone, k)), k
 
 
 def test_linear_ce_gradient_against_differences(T):
@@ -388,7 +414,8 @@ def _flat(sizes, dtype, off, scale=1.0, seed=0):
     return buf, out
 
 
-SIZES = [[1], [0, 5, 0], [8191, 8192, 8193], [1, 2, 3, 5, 7, 100001, 13], [17] * 700, [3000001]]
+SIZES = [[1], [0, 5, 0], [8191, 8192, 8193], [1, 2, 3, 5, 7, 100001, 13], [17] * 700, [3000001],
+         [3, 0, 9001] * 700]  # (the last: more tensors than one launch describes)
 
 
 @pytest.mark.parametrize("sizes", SIZES, ids=lambda s: f"{len(s)}x{max(s)}")
@@ -458,6 +485,35 @@ def test_clip_repeats_and_replays(T):
         T.GradClip([grads[0], grads[0]], 1.0)
 
 
+def test_clip_of_nothing(T):
+    empty = torch.empty(0, device="cuda")
+    call = T.GradClip([empty, empty], 1.0)
+    call.launch()
+    assert float(call.norm) == 0.0 and float(call.coef) == 1.0 and call.check_status() == 0
+
+
+def test_clip_over_a_group(T, monkeypatch):
+    """With a process group the FP64 sum goes through one all-reduce before the scaling (here
+    a stand-in that adds another rank's sum)."""
+    import torch.distributed as dist
+    seen = []
+
+    def all_reduce(x, op=None, group=None):
+        seen.append((x.dtype, x.numel(), group))
+        x += 3.0
+    monkeypatch.setattr(dist, "all_reduce", all_reduce)
+    g = torch.full((100,), 0.1, device="cuda")
+    call = T.GradClip([g], 1.0, outs=[torch.empty_like(g)], group="ranks")
+    call.launch()
+    assert seen == [(torch.float64, 1, "ranks")]
+    norm = (float(g.double().pow(2).sum()) + 3.0) ** 0.5
+    assert abs(float(call.norm) - norm) <= 2.0 ** -21 * norm
+    want = g.double() / (norm + 1e-6)
+    assert bool(((call.outs[0].double() - want).abs() <= 2.0 ** -20 * want).all())
+    with pytest.raises(ValueError, match="current stream"):
+        call.launch(stream=0)
+
+
 def test_clip_in_two_steps(T):
     """dspark_grad_sumsq and dspark_grad_scale, as ranks use them around an all-reduce: two
     halves of a gradient clipped by the norm of the whole equal the whole clipped at once."""
@@ -509,8 +565,8 @@ def test_a_training_step_of_all_of_them(T):
     lce_compare(T_no_weight(ce), ref, H, V)
     want, mag, n = O.embed_grad(ids, ce.dhidden, V, scale)
     want = want + ref["dweight"]
-    rel = 2 * ((H / 16 + 2) + (32 + H / 512 + 2)) * 2.0 ** -23 * ref["reach"] + 2.0 ** -20 + U16
-    tol = (rel + (R / 16 + 2) * 2.0 ** -23) * ref["dw_mag"] + (n[:, None] + 4) * U32 * (mag + ref["dw_mag"])
+    P = 2 * ((H / 16 + 2) + (32 + H / 512 + 2)) * 2.0 ** -23 * ref["reach"] + 2.0 ** -20
+    tol = P * ref["dw_pmag"] + (U16 + (R / 16 + 2) * 2.0 ** -23) * ref["dw_mag"] + (n[:, None] + 4) * U32 * (mag + ref["dw_mag"])
     assert bool(((head.double() - want).abs() <= 1.01 * tol).all())
     norm, coef, clipped = O.clip([head], 0.5)
     assert abs(float(clip.norm) - norm) <= 2.0 ** -21 * norm and coef < 1.0
@@ -534,3 +590,71 @@ def T_no_weight(call):
     c = copy.copy(call)
     c.dweight = None
     return c
+
+
+# ------------------------------------------- hidden gradient gathered by the forward
+@pytest.mark.parametrize("R,V,H,ignored", [(1, 16384, 64, 0), (5, 16400, 72, 5), (100, 20011, 136, 7),
+                                           (128, 16385, 520, 0), (300, 17000, 256, 40), (700, 16640, 1032, 3),
+                                           (8192, 20011, 64, 500)])
+@pytest.mark.parametrize("z_alpha", [0.0, 1e-3])
+def test_linear_ce_gathered_matches_the_statement(T, R, V, H, ignored, z_alpha):
+    """Without a head gradient, from 16384 columns on, the forward gathers the hidden one.
+    The bounds are those of the other way: exponentials are rounded to bf16 instead of dz
+    (relative error 2^-8 of each term; the label's own term is not rounded)."""
+    h, w, t, a = lce_inputs(R, V, H, ignored, seed=R + V + 1)
+    call = T.LinearCE(h, w, t, row_weight=a, z_alpha=z_alpha, dweight=False)
+    assert call.prob.hidden_grad_only == 1
+    call.forward()
+    call.grad_scale.fill_(-0.75)  # known only after the forward
+    call.backward()
+    assert call.check_status() == 0
+    ref = O.linear_ce(h, w, t, a, z_alpha=z_alpha, grad_scale=-0.75)
+    lce_compare(call, ref, H, V)
+    both = T.LinearCE(h, w, t, row_weight=a, z_alpha=z_alpha)
+    both.forward()
+    assert int(both.num_tokens) == int(call.num_tokens)
+    assert abs(float(both.loss_num) - float(call.loss_num)) <= 2.0 ** -18 * abs(float(both.loss_num)) + 1e-30
+    first = [x.clone() for x in (call.loss_num, call.ce_rows, call.lse_rows, call.dhidden)]
+    call.forward()
+    call.backward()
+    assert all(torch.equal(x, y) for x, y in zip(first, (call.loss_num, call.ce_rows, call.lse_rows, call.dhidden)))
+
+
+@pytest.mark.parametrize("R", [60, 200])
+def test_linear_ce_gathered_out_of_the_reference_range(T, R):
+    """A logit past the sampled columns far above every sampled one (by 200 to 1000): the
+    exponentials relative to the sample would overflow, and the call has to go the other way,
+    rows that did not ask for it included.  Then the same buffers with ordinary logits."""
+    V, H = 16500, 16
+    h = torch.zeros(R, H, dtype=torch.bfloat16, device="cuda")
+    w = (torch.randn(V, H, device="cuda") * 0.5).to(torch.bfloat16)
+    w[:, 0] = 0.0
+    w[V - 3, 0] = 200.0
+    w[9000, 0] = 190.0
+    h[:, 1:] = torch.randn(R, H - 1, device="cuda").to(torch.bfloat16)
+    h[::3, 0] = 1.0   # a third of the rows leave the range
+    h[1::3, 0] = 5.0  # a third by far more
+    t = torch.arange(R, device="cuda") * 7 % V
+    t[3] = V - 3
+    call = T.LinearCE(h, w, t, dweight=False)
+    call.grad_scale.fill_(0.5)
+    call.forward()
+    call.backward()
+    assert call.check_status() == 0
+    lce_compare(call, O.linear_ce(h, w, t, grad_scale=0.5), H, V)
+    h[:, 0] = 0.0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call.forward()
+        call.backward()
+    graph.replay()
+    lce_compare(call, O.linear_ce(h, w, t, grad_scale=0.5), H, V)
+    h[::2, 0] = 2.0
+    graph.replay()
+    lce_compare(call, O.linear_ce(h, w, t, grad_scale=0.5), H, V)
+    h[4, 2] = float("nan")
+    call.forward()
+    call.backward()
+    bad = torch.isnan(call.lse_rows)
+    assert bool(bad[4]) and int(bad.sum()) == 1
+    assert not bool(torch.isnan(call.dhidden[torch.arange(R, device="cuda") != 4]).any())

@@ -80,7 +80,7 @@ def _lce_bwd(abi, p, g, ws=0x100000, n=1 << 40):
     (dict(R=0), INVALID), (dict(V=0), INVALID), (dict(H=0), INVALID), (dict(R=-1), INVALID),
     (dict(hidden=0), INVALID), (dict(weight=0), INVALID), (dict(targets=0), INVALID),
     (dict(hidden_ld=56), INVALID), (dict(weight_ld=56), INVALID),
-    (dict(z_alpha=-1.0), INVALID), (dict(z_alpha=float("nan")), INVALID),
+    (dict(hidden_grad_only=2), INVALID), (dict(z_alpha=-1.0), INVALID), (dict(z_alpha=float("nan")), INVALID),
     (dict(H=60), ALIGN), (dict(hidden_ld=68), ALIGN), (dict(weight_ld=68), ALIGN),
     (dict(hidden=0x10008), ALIGN), (dict(weight=0x20002), ALIGN),
     (dict(R=(1 << 24) + 1), UNSUP), (dict(V=(1 << 30) + 1), UNSUP), (dict(H=(1 << 20) + 8), UNSUP),
@@ -113,6 +113,19 @@ def test_lce_refuses_missing_structs_and_workspaces(abi):
 ])
 def test_lce_refuses_bad_gradients(abi, change, status):
     assert _lce_bwd(abi, _lce(abi), _lce_grads(abi, **change)) == status
+
+
+def test_lce_hidden_grad_only(abi):
+    """No head gradient may be asked for, and at a large vocabulary the forward needs the
+    backward's workspace."""
+    assert _lce_bwd(abi, _lce(abi, hidden_grad_only=1), _lce_grads(abi)) == INVALID
+    size = lambda p, g=None: abi.dspark_lce_workspace_size(  # noqa: E731
+        ctypes.byref(p), ctypes.byref(g) if g is not None else None)
+    only = _lce_grads(abi, dweight=0)
+    small, large = _lce(abi, hidden_grad_only=1), _lce(abi, V=20000, hidden_grad_only=1)
+    assert size(small) < size(small, only)
+    assert size(large) == size(large, only) == size(_lce(abi, V=20000), only)
+    assert _lce_fwd(abi, large, n=size(large) - 1) == WS
 
 
 def test_lce_workspace_is_far_below_the_logits(abi):
