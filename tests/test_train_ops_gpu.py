@@ -83,7 +83,7 @@ def lce_compare(call, ref, H, V, g=1.0, base=None):
     (7, 8192, 512, 0), (56, 8192, 512, 9), (64, 257, 72, 0), (65, 255, 136, 1),
     (127, 1000, 200, 3), (128, 1024, 128, 0), (129, 1025, 520, 2), (130, 700, 72, 130),
     (255, 3001, 264, 100), (256, 2048, 256, 0), (257, 777, 1032, 5), (448, 5000, 1024, 205),
-    (1021, 4003, 1000, 100), (2049, 769, 328, 1000),
+    (1021, 4003, 1000, 100), (2049, 769, 328, 1000), (8300, 1500, 64, 5000),
 ])
 @pytest.mark.parametrize("z_alpha", [0.0, 1e-3])
 def test_linear_ce_matches_the_statement(T, R, V, H, ignored, z_alpha):
@@ -113,6 +113,22 @@ def test_linear_ce_over_several_pieces(T):
     call.backward()
     assert call.check_status() == 0
     lce_compare(call, O.linear_ce(h, w, t, a), H, V)
+
+
+def test_linear_ce_split_and_in_pieces(T):
+    """Few row tiles, so the hidden gradient's K range is split, and two pieces, the second
+    shorter: every split's plane is added to."""
+    R, V, H = 1024, 140003, 64
+    h, w, t, a = lce_inputs(R, V, H, 300, seed=11)
+    call = T.LinearCE(h, w, t, row_weight=a)
+    call.forward()
+    call.backward()
+    ref = O.linear_ce(h, w, t, a)
+    lce_compare(call, ref, H, V)
+    gathered = T.LinearCE(h, w, t, row_weight=a, dweight=False)
+    gathered.forward()
+    gathered.backward()
+    lce_compare(gathered, ref, H, V)
 
 
 @pytest.mark.parametrize("R", [40, 300])
@@ -335,7 +351,8 @@ def test_embedding_matches_the_statement(T, R, Vt, D, dtype):
     assert call.check_status() == 3 and bool((out[0, :D] == 0).all())
 
 
-@pytest.mark.parametrize("R,Vt,D", EMB + [(40000, 11, 64), (70001, 151936, 16)])
+@pytest.mark.parametrize("R,Vt,D", EMB + [(40000, 11, 64), (70001, 151936, 16), (50, 300001, 8), (5000, 300001, 8),
+                                          (140001, 300001, 8), (140001, 97, 40)])
 @pytest.mark.parametrize("dtype,grad", [(torch.bfloat16, torch.float32), (torch.bfloat16, torch.bfloat16),
                                         (torch.float32, torch.float32), (torch.float32, torch.bfloat16)])
 @pytest.mark.parametrize("hot", [0.0, 0.4])
