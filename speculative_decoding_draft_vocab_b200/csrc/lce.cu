@@ -1,10 +1,11 @@
 // Linear cross entropy: softmax cross entropy of z = hidden . weight^T over the whole
-// vocabulary and its gradients, the logits never kept.
+// vocabulary and its gradients, in a workspace that does not grow with the logits.
 //   forward   prep:  the labelled rows' places, their hidden rows gathered compact
 //             fwd:   product tiles; each row's (maximum, sum of exponentials) in the tile
 //             merge: logsumexp, CE and the loss from the tiles' pairs
 //   backward, a piece of the vocabulary at a time:
-//             dz:    the product again; dL/dz of the piece, bf16
+//             dz:    dL/dz of the piece, bf16: from the product again, or from the logits
+//                    where they are few enough to have stayed in the workspace
 //             dw:    dweight rows of the piece = dz^T . hidden
 //             dh:    partial sums of dhidden = dz . weight, FP32
 //             then dhidden from the partial sums, scattered to the labelled rows
@@ -181,7 +182,7 @@ __device__ __forceinline__ Item decode(const Work& wk, int w, int me, int kch, i
   return it;
 }
 
-enum : int { kFwd = 0, kDz = 1, kDh = 2, kDwBf16 = 3, kDwF32 = 4, kGather = 5 };
+enum : int { kFwd = 0, kDz = 1, kDh = 2, kDwBf16 = 3, kDwF32 = 4, kGather = 5, kFwdKeep = 6 };
 
 struct EpiArgs {
   View ws;
@@ -440,11 +441,11 @@ __device__ __forceinline__ void gather_finish(const EpiArgs& a, const CUtensorMa
       make_float2(ref, (s4[0] + s4[1]) + (s4[2] + s4[3]));
 }
 
-// FP32 results: dhidden's partial sums (one plane per K split; a plane's element gets one
+// FP32 results: kept logits, dhidden's partial sums (one plane per K split; a plane's element gets one
 // addition per piece, in stream order, so the sums have a fixed order), or dweight.
 template <int EPI>
 __device__ __forceinline__ void f32_finish(const EpiArgs& a, const CUtensorMap& out, Share& sh, const float (&z)[128]) {
-  if (sh.m0 >= (EPI == kDh ? sh.n_valid : a.rows) || (sh.empty && a.add)) return;
+  if (sh.m0 >= (EPI == kDh || EPI == kFwdKeep ? sh.n_valid : a.rows) || (sh.empty && a.add)) return;
 #pragma unroll
   for (int c = 0; c < 128; c += 32) {
     if (c >= sh.cols || sh.n0 + sh.c0 + c >= a.n_cols) break;
@@ -475,13 +476,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmO, const Work wk, const EpiArgs ea, const int bn) {
   constexpr bool A_MN = EPI == kDwBf16 || EPI == kDwF32;
-  constexpr bool B_MN = EPI != kFwd && EPI != kDz && EPI != kGather;
+  constexpr bool B_MN = EPI == kDh || A_MN;
   constexpr int STAGES = stages<CG>(EPI);
   // The tensor cores' FP32 accumulation rounds towards zero: over K = 4096 the logits come
   // out 2.2e-6 short (relative), over K = 512 3e-7.  The forward hands over its accumulator
   // every 512 values of K and the epilogue adds the segments in registers, rounding to
   // nearest; the other products are rounded to bf16 right after, where it does not show.
-  constexpr int SEG = EPI == kFwd || EPI == kGather ? 512 / BK : 1 << 29;
+  constexpr bool SEGMENTED = EPI == kFwd || EPI == kFwdKeep || EPI == kGather;
+  constexpr int SEG = SEGMENTED ? 512 / BK : 1 << 29;
   constexpr uint32_t SA = kBM * BK * 2, SS = stage_bytes<CG>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -631,7 +633,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const Item t = decode(wk, w, me, kch, ks);
       sh.m0 = (t.mt * CG + int(rank)) * kBM + q * 32, sh.n0 = t.nt * bn;
       sh.nt = t.nt, sh.plane0 = t.s * me * kBM * CG, sh.empty = t.kc0 == t.kc1;
-      if constexpr (EPI == kFwd || EPI == kGather) {
+      if constexpr (SEGMENTED) {
         float z[128];
 #pragma unroll
           for (int i = 0; i < 128; ++i) z[i] = 0.f;
@@ -651,8 +653,9 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           }
           release(b);
         }
-        if constexpr (EPI == kFwd) fwd_finish(ea, sh, z);
-        else gather_finish(ea, tmO, sh, z);
+        if constexpr (EPI == kGather) gather_finish(ea, tmO, sh, z);
+        else fwd_finish(ea, sh, z);
+        if constexpr (EPI == kFwdKeep) f32_finish<EPI>(ea, tmO, sh, z);
       } else {
         const int b = tl & 1;
         if (!mbar_wait_bounded(accf0 + 8 * b, uint32_t(tl >> 1) & 1u)) timed_out = true;
@@ -778,6 +781,39 @@ __global__ void __launch_bounds__(kSlices * 32) merge_kernel(const View ws, cons
   }
 }
 
+// ------------------------------------------------------------------ dz of kept logits
+// As dz_finish, from the logits that the forward kept: eight columns per thread.  Rows up to a
+// whole 64-row K chunk and columns up to a whole 64-column one are zeros.
+__global__ void __launch_bounds__(256) dz_kernel(const View ws, const Plan pl, const float z_alpha,
+                                                 const float* grad_scale) {
+  pdl_wait();
+  pdl_trigger();
+  const int n = ws.hdr->n_valid, rows = (n + 63) / 64 * 64;
+  const int c8 = int((pl.V + 63) / 64 * 8);
+  const float g = grad_scale ? *grad_scale : 1.f;
+  for (int i = blockIdx.y; i < rows; i += gridDim.y) {
+    const bool live = i < n;
+    const int tgt = live ? ws.tok[i] : -1;
+    const float lse2 = live ? ws.lse2[i] : 0.f, gw = live ? g * ws.w[i] : 0.f;
+    const float scale = gw * fmaf(2.f * z_alpha, lse2 * kLn2, 1.f);
+    const float4* src = reinterpret_cast<const float4*>(ws.z + size_t(i) * pl.piece);
+    uint4* dst = reinterpret_cast<uint4*>(ws.dz + size_t(i) * pl.piece);
+    for (int j = int(blockIdx.x) * 256 + threadIdx.x; j < c8; j += int(gridDim.x) * 256) {
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (live) {
+        const float4 a = __ldcs(src + 2 * j), b = __ldcs(src + 2 * j + 1);
+        const float z[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float p = ex2(fmaf(z[u], kLog2e, -lse2)) * scale;
+          v[u] = 8 * j + u >= pl.V ? 0.f : 8 * j + u == tgt ? p - gw : p;
+        }
+      }
+      dst[j] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    }
+  }
+}
+
 // ------------------------------------------------------------------ reference
 // A gathered row's reference: the largest logit of the sampled columns (one that is not a
 // number, or infinite, is left to the exponentials to show).
@@ -883,8 +919,8 @@ cudaError_t launch_merge(const dspark_lce_problem_t& p, const dspark_lce_out_t& 
 // The forward product over the first `cols` columns, then the rows' logsumexps (all columns)
 // or references (a sample of them).
 cudaError_t launch_logsumexp(const dspark_lce_problem_t& p, const dspark_lce_out_t& out, const Plan& pl, const View& ws,
-                             int64_t cols, bool if_redo, cudaStream_t s) {
-  CUtensorMap ma, mb;
+                             int64_t cols, bool keep, bool if_redo, cudaStream_t s) {
+  CUtensorMap ma, mb, mo;
   if (!tc::make_map(&ma, ws.hsup, pl.Rp, p.H, p.H, 64, kBM) ||
       !tc::make_map(&mb, p.weight, p.V, p.H, p.weight_ld, 64, kBN / pl.cg))
     return cudaErrorInvalidValue;
@@ -895,7 +931,9 @@ cudaError_t launch_logsumexp(const dspark_lce_problem_t& p, const dspark_lce_out
   ea.rows = int32_t(pl.Rp);
   ea.n_cols = int32_t(cols);
   ea.if_redo = if_redo;
-  const cudaError_t e = product<kFwd>(pl, ma, mb, ma, wk, ea, kBN, s);
+  if (keep && !tc::make_out_map(&mo, ws.z, pl.Rp, pl.piece, pl.piece)) return cudaErrorInvalidValue;
+  const cudaError_t e = keep ? product<kFwdKeep>(pl, ma, mb, mo, wk, ea, kBN, s)
+                             : product<kFwd>(pl, ma, mb, ma, wk, ea, kBN, s);
   if (e != cudaSuccess) return e;
   if (cols == p.V) return launch_merge(p, out, pl, ws, if_redo, s);
   PdlLaunch l(ceil_div(p.R, 256), 256, 0, s);
@@ -930,8 +968,15 @@ cudaError_t launch_pieces(const dspark_lce_problem_t& p, const dspark_lce_grads_
     ea.grad_scale = g.grad_scale;
     ea.if_redo = pl.gathered && what == kDz;
     const Work wz = make_work(tiles(p.R, kBM * pl.cg), tiles(n, kBN), tiles(p.H, BK), 16, false, ws);
-    e = what == kGather ? product<kGather>(pl, h_k, w_k, z_out, wz, ea, kBN, s)
-                        : product<kDz>(pl, h_k, w_k, z_out, wz, ea, kBN, s);
+    if (what == kDz && pl.keep) {
+      const int64_t x = std::min<int64_t>(ceil_div(p.V, 2048), 64), y = std::min<int64_t>(pl.Rp, ceil_div(16 * kSlots, x));
+      PdlLaunch l(x, 256, 0, s);
+      l.cfg.gridDim.y = unsigned(y);
+      e = cudaLaunchKernelEx(&l.cfg, dz_kernel, ws, pl, p.z_alpha, g.grad_scale);
+    } else {
+      e = what == kGather ? product<kGather>(pl, h_k, w_k, z_out, wz, ea, kBN, s)
+                          : product<kDz>(pl, h_k, w_k, z_out, wz, ea, kBN, s);
+    }
     if (e != cudaSuccess) return e;
     if (g.dweight) {
       void* d0 = static_cast<uint8_t*>(g.dweight) + size_t(v0) * g.dweight_ld * (f32 ? 4 : 2);
@@ -965,21 +1010,21 @@ cudaError_t launch_pieces(const dspark_lce_problem_t& p, const dspark_lce_grads_
 }  // namespace
 
 cudaError_t launch_fwd(const dspark_lce_problem_t& p, const dspark_lce_out_t& out, const Plan& pl, const View& ws,
-                       cudaStream_t s) {
+                       bool keep, cudaStream_t s) {
   const int64_t ctas = std::min<int64_t>(p.R, 4 * kSlots);
   const int64_t rows_per_cta = ceil_div(p.R, ctas);
   PdlLaunch first(ceil_div(p.R, rows_per_cta), kPrepThreads, 0, s);
   first.cfg.numAttrs = 0;  // the first kernel of the call waits for all work before it
   cudaError_t e = cudaLaunchKernelEx(&first.cfg, prep_kernel, p, ws, out.num_tokens, rows_per_cta);
   if (e != cudaSuccess) return e;
-  if (!pl.gathered) return launch_logsumexp(p, out, pl, ws, p.V, false, s);
+  if (!pl.gathered) return launch_logsumexp(p, out, pl, ws, p.V, keep, false, s);
   // the reference from a few columns, then the logsumexp and the hidden gradient in one pass
-  if ((e = launch_logsumexp(p, out, pl, ws, kSampleCols, false, s)) != cudaSuccess) return e;
+  if ((e = launch_logsumexp(p, out, pl, ws, kSampleCols, false, false, s)) != cudaSuccess) return e;
   dspark_lce_grads_t none{};
   if ((e = launch_pieces(p, none, pl, ws, kGather, true, s)) != cudaSuccess) return e;
   if ((e = launch_merge(p, out, pl, ws, false, s)) != cudaSuccess) return e;
   // and where a row left the range of its reference, both again from its own maximum
-  if ((e = launch_logsumexp(p, out, pl, ws, p.V, true, s)) != cudaSuccess) return e;
+  if ((e = launch_logsumexp(p, out, pl, ws, p.V, false, true, s)) != cudaSuccess) return e;
   return launch_pieces(p, none, pl, ws, kDz, true, s);
 }
 

@@ -15,6 +15,9 @@ constexpr size_t kPieceBytes = size_t(256) << 20;    // bound on the kept piece 
 constexpr int kMaxSplitTiles = 32;                   // more row tiles than this are not split
 constexpr int kMaxSplit = 32;
 constexpr size_t kPlaneBytes = size_t(96) << 20;     // bound on split planes (they stay in L2)
+// The logits of a problem whose FP32 logits take no more than this stay in the workspace for
+// the backward (at 448 rows of 151936 columns 260 MiB), which is then spared a product.
+constexpr size_t kKeepBytes = size_t(320) << 20;
 // A gathered forward takes the reference of a row's exponentials from this many columns.
 constexpr int kSampleCols = 2048;
 // From this vocabulary on it pays: it saves one of three products and adds the sample.
@@ -42,6 +45,7 @@ struct Plan {
   int64_t plane_rows;  // rows of the hidden gradient's partial sums, all planes together
   uint8_t ksplit[kMaxSplitTiles + 1];  // its K splits (planes) by the number of row tiles
   int64_t merge_blocks;
+  int keep;            // the logits stay in the workspace where it has room for a backward
   int gathered;        // the forward also gathers the hidden gradient (no head gradient follows)
 };
 
@@ -56,6 +60,7 @@ struct View {
   float* ref;          // [R] base-2 exponent that a gathered row's exponentials are relative to
   uint16_t* hsup;      // [Rp][H] bf16 labelled hidden rows, compact, zeros up to a whole chunk
   float2* part;        // [2 fwd_tiles][Rp] (base-2 maximum, sum) of a row's columns in half a tile
+  float* z;            // [Rp][piece] kept logits
   uint16_t* dz;        // [Rp][piece] bf16 piece of dL/dlogits
   float* planes;       // [splits][row tiles' rows][H] partial sums of the hidden gradient
 };
@@ -92,6 +97,7 @@ inline Plan make_plan(int64_t R, int64_t V, int64_t H, bool hidden_grad_only) {
   }
   p.merge_blocks = ceil_div(R, kMergeRows);
   p.gathered = hidden_grad_only && V >= kGatherFrom;
+  p.keep = !p.gathered && p.pieces == 1 && 4 * size_t(p.Rp) * size_t(p.piece) <= kKeepBytes;
   return p;
 }
 
@@ -101,7 +107,7 @@ __host__ __device__ inline int splits_of(const Plan& p, int row_tiles) {
 }
 
 struct Offsets {
-  size_t hdr, loss_part, index, tok, w, lse2, zt, ref, hsup, part, dz, planes, bytes;
+  size_t hdr, loss_part, index, tok, w, lse2, zt, ref, hsup, part, z, dz, planes, bytes;
 };
 
 inline Offsets offsets(const Plan& p, bool bwd, bool dhidden) {
@@ -120,6 +126,7 @@ inline Offsets offsets(const Plan& p, bool bwd, bool dhidden) {
   take(o.ref, 4 * R);
   take(o.hsup, 2 * Rp * size_t(p.H));
   take(o.part, sizeof(float2) * 2 * size_t(p.fwd_tiles) * Rp);
+  take(o.z, bwd && p.keep ? 4 * Rp * size_t(p.piece) : 0);
   take(o.dz, bwd ? 2 * Rp * size_t(p.piece) : 0);
   take(o.planes, bwd && dhidden ? sizeof(float) * size_t(p.plane_rows) * size_t(p.H) : 0);
   o.bytes = off;
@@ -140,13 +147,15 @@ inline View view(void* base, const Plan& p) {
   v.ref = reinterpret_cast<float*>(b + o.ref);
   v.hsup = reinterpret_cast<uint16_t*>(b + o.hsup);
   v.part = reinterpret_cast<float2*>(b + o.part);
+  v.z = reinterpret_cast<float*>(b + o.z);
   v.dz = reinterpret_cast<uint16_t*>(b + o.dz);
   v.planes = reinterpret_cast<float*>(b + o.planes);
   return v;
 }
 
+// `keep`: the workspace holds the plan's kept logits.
 cudaError_t launch_fwd(const dspark_lce_problem_t& p, const dspark_lce_out_t& out, const Plan& plan, const View& ws,
-                       cudaStream_t s);
+                       bool keep, cudaStream_t s);
 cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& g, const Plan& plan, const View& ws,
                        cudaStream_t s);
 

@@ -94,7 +94,10 @@ dspark_status_t dspark_lce_fwd(const dspark_lce_problem_t* prob, const dspark_lc
   if (st != DSPARK_OK) return st;
   if ((st = check_ws(ws, ws_bytes, dspark_lce_workspace_size(prob, nullptr))) != DSPARK_OK) return st;
   const lce::Plan plan = lce_plan(prob);
-  return cuda_status(lce::launch_fwd(*prob, *out, plan, lce::view(ws, plan), reinterpret_cast<cudaStream_t>(stream)));
+  // a workspace that a backward could use is one that a backward may follow on
+  const bool keep = plan.keep && ws_bytes >= lce::offsets(plan, true, false).bytes;
+  return cuda_status(
+      lce::launch_fwd(*prob, *out, plan, lce::view(ws, plan), keep, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 dspark_status_t dspark_lce_bwd(const dspark_lce_problem_t* prob, const dspark_lce_grads_t* grads, void* ws,

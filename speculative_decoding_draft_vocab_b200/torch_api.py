@@ -453,8 +453,8 @@ class _DeviceCall:
 
 class LinearCE(_DeviceCall):
     """A prepared linear cross entropy: the loss of ``hidden @ weight.T`` against
-    ``targets`` over the whole vocabulary and its gradients, the logits never kept
-    (dspark_lce_fwd, dspark_lce_bwd).
+    ``targets`` over the whole vocabulary and its gradients, in a workspace that does not grow
+    with the logits (dspark_lce_fwd, dspark_lce_bwd).
 
     ``hidden`` [R, H] and ``weight`` [V, H] are bf16 with contiguous rows, ``targets`` [R]
     int64, ``row_weight`` [R] fp32.  forward() writes ``loss_num``, ``num_tokens``,

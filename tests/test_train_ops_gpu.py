@@ -131,6 +131,20 @@ def test_linear_ce_split_and_in_pieces(T):
     lce_compare(gathered, ref, H, V)
 
 
+@pytest.mark.parametrize("R,V,kept", [(448, 151936, True), (600, 151936, False)])
+def test_linear_ce_kept_logits_or_not(T, R, V, kept):
+    """On both sides of the bound up to which the logits stay in the workspace; the same rows'
+    gradients agree to the bounds of either."""
+    H = 64
+    h, w, t, a = lce_inputs(R, V, H, 100, seed=12)
+    call = T.LinearCE(h, w, t, row_weight=a, z_alpha=1e-3)
+    assert (call.ws.numel() > 4 * R * V) == kept
+    call.forward()
+    call.backward()
+    assert call.check_status() == 0
+    lce_compare(call, O.linear_ce(h, w, t, a, z_alpha=1e-3), H, V)
+
+
 @pytest.mark.parametrize("R", [40, 300])
 def test_linear_ce_strides_scores_and_partial_gradients(T, R):
     V, H = 1003, 144
