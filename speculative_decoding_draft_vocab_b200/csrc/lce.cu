@@ -548,6 +548,8 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     // ---------------- TMA producer: this CTA's 128 rows of A, its 1/CG of B's columns
     const int bnc = bn / CG;
     const uint32_t tx = CG * (SA + uint32_t(bnc) * BK * 2);
+    // operands that the kernels before wrote by ordinary stores (the gathered rows, dz)
+    asm volatile("fence.proxy.async.global;" ::: "memory");
     int it = 0;
     for (int w = tile0; w < W; w += tiles_step) {
       const Item t = decode(wk, w, me, kch, ks);
@@ -593,10 +595,10 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           tc::fence_after_sync();
           const uint32_t sa = smem_u32(smem + size_t(st) * SS), sb = sa + SA;
 #pragma unroll
-          for (int ks = 0; ks < BK / 16; ++ks) {
-            const uint64_t ad = A_MN ? tc::sdesc(sa + ks * 2048, 8192, 1024) : tc::sdesc(sa + ks * 32, 16, 1024);
-            const uint64_t bd = B_MN ? tc::sdesc(sb + ks * 2048, 8192, 1024) : tc::sdesc(sb + ks * 32, 16, 1024);
-            mma<CG>(d_tmem, ad, bd, idesc, (kc > kfirst || ks > 0) ? 1u : 0u);
+          for (int k = 0; k < BK / 16; ++k) {
+            const uint64_t ad = A_MN ? tc::sdesc(sa + k * 2048, 8192, 1024) : tc::sdesc(sa + k * 32, 16, 1024);
+            const uint64_t bd = B_MN ? tc::sdesc(sb + k * 2048, 8192, 1024) : tc::sdesc(sb + k * 32, 16, 1024);
+            mma<CG>(d_tmem, ad, bd, idesc, (kc > kfirst || k > 0) ? 1u : 0u);
           }
           commit<CG>(empty0 + 8 * st);  // frees the stage once these MMAs have read it
         }
@@ -636,7 +638,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       if constexpr (SEGMENTED) {
         float z[128];
 #pragma unroll
-          for (int i = 0; i < 128; ++i) z[i] = 0.f;
+        for (int i = 0; i < 128; ++i) z[i] = 0.f;
         for (int kc = t.kc0; kc < t.kc1; kc += SEG, ++tl) {
           const int b = tl & 1;
           if (!mbar_wait_bounded(accf0 + 8 * b, uint32_t(tl >> 1) & 1u)) timed_out = true;
