@@ -70,43 +70,114 @@ __device__ void check_ids(const dspark_embed_problem_t& p, WsEmbedHeader* hdr) {
 }
 
 // ------------------------------------------------------------------ lookup
-// A warp takes one row's run of 2 x 32 16-byte vectors at a time; the last CTA checks the ids.
-constexpr int kFwdVecs = 2;
+// Whether the ids are checked by one CTA more, beside the lookup (its time, about 1.2 us per
+// 2048 rows, is then hidden by rows of 2 KB and more, or short anyway), or by the lookup's own
+// threads, behind a kernel that clears the status word.
+inline bool check_beside(const dspark_embed_problem_t& p) {
+  return p.R <= 8192 || p.D * (p.dtype == DSPARK_F32 ? 4 : 2) >= 2048;
+}
+
+__global__ void clear_status_kernel(WsEmbedHeader* hdr) {
+  pdl_trigger();
+  if (threadIdx.x == 0) hdr->status = 0u;
+}
 
 template <bool F32>
-__global__ void __launch_bounds__(256, 8) lookup_kernel(const FwdArgs a) {
-  if (blockIdx.x == gridDim.x - 1) {
+__device__ __forceinline__ uint4 scaled(const uint4& q, float scale) {
+  using V = Vec<F32>;
+  float v[V::N];
+  V::get(q, v);
+#pragma unroll
+  for (int i = 0; i < V::N; ++i) v[i] *= scale;
+  return V::put(v);
+}
+
+// Rows of 32 vectors and more: a warp takes one row's run of 2 x 32 16-byte vectors at a time.
+// Shorter rows: a thread takes two vectors, wherever in the rows they fall, so that no lane
+// idles.
+constexpr int kFwdVecs = 2;
+
+template <bool F32, bool NARROW>
+__global__ void __launch_bounds__(256, 8) lookup_kernel(const FwdArgs a, const int beside) {
+  if (beside && blockIdx.x == gridDim.x - 1) {
     check_ids(a.p, a.hdr);
     return;
   }
+  pdl_wait();
   using V = Vec<F32>;
-  const int lane = threadIdx.x & 31;
-  const int64_t nv = a.p.D / V::N, parts = (nv + 32 * kFwdVecs - 1) / (32 * kFwdVecs);
-  const int64_t items = a.p.R * parts, step = int64_t(gridDim.x - 1) * 8;
-  for (int64_t w = int64_t(blockIdx.x) * 8 + threadIdx.x / 32; w < items; w += step) {
-    const int64_t r = w / parts, j0 = (w - r * parts) * 32 * kFwdVecs + lane;
+  const int ctas = int(gridDim.x) - beside;
+  const int64_t nv = a.p.D / V::N, ldt = a.table_ld / V::N, ldo = a.out_ld / V::N;
+  const uint4* table = static_cast<const uint4*>(a.table);
+  uint4* out = static_cast<uint4*>(a.out);
+  // the row's place in the table, or -1; its first thread reports an id outside
+  auto place = [&](int64_t r, bool first) -> int64_t {
     const int64_t id = a.p.ids[r];
-    const bool live = !dropped(a.p, r) && in_table(a.p, id);
-    const uint4* src = static_cast<const uint4*>(a.table) + (live ? id : 0) * (a.table_ld / V::N);
-    uint4* dst = static_cast<uint4*>(a.out) + r * (a.out_ld / V::N);
-    uint4 q[kFwdVecs];
+    if (dropped(a.p, r)) return -1;
+    if (in_table(a.p, id)) return id;
+    if (!beside && first) atomicOr(&a.hdr->status, kFlagIdOutOfRange);
+    return -1;
+  };
+  if constexpr (NARROW) {
+    const int64_t total = a.p.R * nv, step = int64_t(ctas) * 256;
+    const uint32_t n = uint32_t(nv);
+    for (int64_t i0 = int64_t(blockIdx.x) * 256 + threadIdx.x; i0 < total; i0 += kFwdVecs * step) {
+      uint4 q[kFwdVecs];
+      int64_t to[kFwdVecs];
 #pragma unroll
-    for (int k = 0; k < kFwdVecs; ++k)
-      if (live && j0 + 32 * k < nv) q[k] = src[j0 + 32 * k];
-#pragma unroll
-    for (int k = 0; k < kFwdVecs; ++k) {
-      if (j0 + 32 * k >= nv) break;
-      uint4 o = make_uint4(0u, 0u, 0u, 0u);
-      if (live) {
-        float v[V::N];
-        V::get(q[k], v);
-#pragma unroll
-        for (int i = 0; i < V::N; ++i) v[i] *= a.p.scale;
-        o = V::put(v);
+      for (int k = 0; k < kFwdVecs; ++k) {
+        const int64_t i = i0 + k * step;
+        q[k] = make_uint4(0u, 0u, 0u, 0u);
+        to[k] = -1;
+        if (i >= total) continue;
+        const int64_t r = uint32_t(i) / n, j = i - r * n;  // total is below 2^29: rows below 2^24, vectors below 32
+        const int64_t id = place(r, j == 0);
+        to[k] = r * ldo + j;
+        if (id >= 0) q[k] = table[id * ldt + j];
       }
-      __stcs(dst + j0 + 32 * k, o);  // written once: the table's rows keep their place in L2
+#pragma unroll
+      for (int k = 0; k < kFwdVecs; ++k)
+        if (to[k] >= 0) __stcs(out + to[k], scaled<F32>(q[k], a.p.scale));
+    }
+  } else {
+    const int lane = threadIdx.x & 31;
+    const int64_t parts = (nv + 32 * kFwdVecs - 1) / (32 * kFwdVecs);
+    const int64_t items = a.p.R * parts, step = int64_t(ctas) * 8;
+    for (int64_t w = int64_t(blockIdx.x) * 8 + threadIdx.x / 32; w < items; w += step) {
+      const int64_t r = w / parts, j0 = (w - r * parts) * 32 * kFwdVecs + lane;
+      const int64_t id = place(r, j0 == 0);
+      const bool live = id >= 0;
+      const uint4* src = table + (live ? id : 0) * ldt;
+      uint4* dst = out + r * ldo;
+      uint4 q[kFwdVecs];
+#pragma unroll
+      for (int k = 0; k < kFwdVecs; ++k)
+        if (live && j0 + 32 * k < nv) q[k] = src[j0 + 32 * k];
+#pragma unroll
+      for (int k = 0; k < kFwdVecs; ++k) {
+        if (j0 + 32 * k >= nv) break;
+        const uint4 o = live ? scaled<F32>(q[k], a.p.scale) : make_uint4(0u, 0u, 0u, 0u);
+        __stcs(dst + j0 + 32 * k, o);  // written once: the table's rows keep their place in L2
+      }
     }
   }
+}
+
+template <bool F32>
+cudaError_t lookup(const FwdArgs& a, cudaStream_t s) {
+  const int64_t nv = a.p.D / Vec<F32>::N;
+  const bool narrow = nv < 32, beside = check_beside(a.p);
+  const int64_t parts = (nv + 32 * kFwdVecs - 1) / (32 * kFwdVecs);
+  const int64_t work = narrow ? (a.p.R * nv + 511) / 512 : (a.p.R * parts + 7) / 8;
+  PdlLaunch l(std::min<int64_t>(work, 148 * 8) + beside, 256, 0, s);
+  if (beside) {
+    l.cfg.numAttrs = 0;  // the call's only kernel: after all work before it
+  } else {
+    clear_status_kernel<<<1, 32, 0, s>>>(a.hdr);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return narrow ? cudaLaunchKernelEx(&l.cfg, lookup_kernel<F32, true>, a, int(beside))
+                : cudaLaunchKernelEx(&l.cfg, lookup_kernel<F32, false>, a, int(beside));
 }
 
 // ------------------------------------------------------------------ zero rows
@@ -663,12 +734,7 @@ cudaError_t sums(const BwdArgs& a, const uint32_t* key, const uint32_t* row, cud
 }  // namespace
 
 cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t s) {
-  const bool f32 = a.p.dtype == DSPARK_F32;
-  const int64_t nv = a.p.D / (f32 ? 4 : 8), parts = (nv + 32 * kFwdVecs - 1) / (32 * kFwdVecs);
-  const int64_t ctas = std::min<int64_t>((a.p.R * parts + 7) / 8, 148 * 8);
-  if (f32) lookup_kernel<true><<<unsigned(ctas + 1), 256, 0, s>>>(a);
-  else lookup_kernel<false><<<unsigned(ctas + 1), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return a.p.dtype == DSPARK_F32 ? lookup<true>(a, s) : lookup<false>(a, s);
 }
 
 cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t s) {

@@ -343,7 +343,7 @@ EMB = [(1, 1, 8), (1, 100, 64), (5, 3, 8), (33, 50, 24), (448, 5000, 264), (1000
        (4097, 100000, 32), (9001, 600, 1032)]
 
 
-@pytest.mark.parametrize("R,Vt,D", EMB)
+@pytest.mark.parametrize("R,Vt,D", EMB + [(8193, 50, 8), (20003, 300, 248), (9001, 100, 264), (70001, 1000, 40)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_embedding_matches_the_statement(T, R, Vt, D, dtype):
     g = torch.Generator(device="cuda").manual_seed(R + D)
@@ -359,10 +359,14 @@ def test_embedding_matches_the_statement(T, R, Vt, D, dtype):
     # the product in FP32, then the type's rounding
     assert bool(((out[:, :D].double() - ref).abs() <= (U32 + _u(dtype)) * 1.01 * ref.abs()).all())
     assert bool((out[:, D:] == 3.0).all())
-    ids[0] = Vt
-    valid[0] = 1
+    last = R - 1
+    ids[last] = Vt
+    valid[last] = 1
     call.launch()
-    assert call.check_status() == 3 and bool((out[0, :D] == 0).all())
+    assert call.check_status() == 3 and bool((out[last, :D] == 0).all())
+    valid[last] = 0  # the status is the last call's
+    call.launch()
+    assert call.check_status() == 0
 
 
 @pytest.mark.parametrize("R,Vt,D", EMB + [(40000, 11, 64), (70001, 151936, 16), (50, 300001, 8), (5000, 300001, 8),
