@@ -581,7 +581,8 @@ __device__ __forceinline__ int64_t lower_bound(const uint32_t* key, int64_t n, u
   return lo;
 }
 
-// A warp zeroes those of 32 table rows, from `r0` and below `r1`, that no sorted key names.
+// A warp zeroes those of at most 32 table rows, from `r0` and below `r1`, that no sorted key
+// names.
 template <bool TF32>
 __device__ void zero_untouched(const BwdArgs& a, const uint32_t* key, int64_t r0, int64_t r1, int lane) {
   constexpr int N = Vec<TF32>::N;
@@ -615,8 +616,9 @@ __global__ void __launch_bounds__(256) sum_kernel(const BwdArgs a, const uint32_
   const uint32_t none = uint32_t(a.p.Vt);
   const int64_t w = int64_t(blockIdx.x) * 8 + threadIdx.x / 32;
   if (w >= a.plan.windows * blocks) {
-    const int64_t r0 = a.plan.fill + (w - a.plan.windows * blocks) * 32;
-    if (!a.accumulate && r0 < a.p.Vt) zero_untouched<TF32>(a, key, r0, a.p.Vt, lane);
+    const int64_t r0 = a.plan.fill + (w - a.plan.windows * blocks) * a.plan.zero_rows;
+    if (!a.accumulate && r0 < a.p.Vt)
+      zero_untouched<TF32>(a, key, r0, min(r0 + a.plan.zero_rows, a.p.Vt), lane);
     return;
   }
   const int64_t win = w / blocks, j = (w - win * blocks) * 32 + lane;
@@ -673,13 +675,20 @@ __global__ void __launch_bounds__(256) sum_kernel(const BwdArgs a, const uint32_
   else write_row<TF32, N>(a, cur, j * N, acc);
 }
 
+// (volatile: the compiler would sink each load to its addition and wait for one at a time)
+__device__ __forceinline__ float4 load_part(const float* p) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
 // The segments that cross windows: the window a segment begins in adds the parts that the
 // windows after it left.
 template <bool F32, bool TF32>
 __global__ void __launch_bounds__(256) join_kernel(const BwdArgs a, const uint32_t* key) {
   pdl_wait();
   pdl_trigger();
-  constexpr int N = Vec<F32>::N, U = F32 ? 32 : 16;  // parts in flight
+  constexpr int N = Vec<F32>::N, U = F32 ? 16 : 8;  // parts in flight
   const int lane = threadIdx.x & 31;
   const int64_t nv = a.p.D / N, blocks = (nv + 31) / 32;
   const int64_t w = int64_t(blockIdx.x) * 8 + threadIdx.x / 32;
@@ -710,12 +719,14 @@ __global__ void __launch_bounds__(256) join_kernel(const BwdArgs a, const uint32
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int i = 0; i < N / 4; ++i)
-        f[u][i] = x + u <= last ? *reinterpret_cast<const float4*>(q + u * stride + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        f[u][i] = load_part(q + (x + u <= last ? u : 0) * stride + 4 * i);  // (past the last: not added)
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      if (x + u > last) break;
 #pragma unroll
       for (int i = 0; i < N / 4; ++i)
         acc[4 * i] += f[u][i].x, acc[4 * i + 1] += f[u][i].y, acc[4 * i + 2] += f[u][i].z, acc[4 * i + 3] += f[u][i].w;
+    }
   }
   write_row<TF32, N>(a, id, j * N, acc);
 }
@@ -723,7 +734,7 @@ __global__ void __launch_bounds__(256) join_kernel(const BwdArgs a, const uint32
 template <bool F32, bool TF32>
 cudaError_t sums(const BwdArgs& a, const uint32_t* key, const uint32_t* row, cudaStream_t s) {
   const int64_t nv = a.p.D / Vec<F32>::N, warps = a.plan.windows * ((nv + 31) / 32);
-  const int64_t zeros = a.accumulate ? 0 : (a.p.Vt - a.plan.fill + 31) / 32;
+  const int64_t zeros = a.accumulate ? 0 : (a.p.Vt - a.plan.fill + a.plan.zero_rows - 1) / a.plan.zero_rows;
   PdlLaunch l((warps + zeros + 7) / 8, 256, 0, s);
   cudaError_t e = cudaLaunchKernelEx(&l.cfg, sum_kernel<F32, TF32>, a, key, row);
   if (e != cudaSuccess) return e;

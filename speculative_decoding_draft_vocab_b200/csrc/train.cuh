@@ -34,6 +34,7 @@ struct Plan {
   int window;          // sorted rows per partial sum
   int64_t windows;
   int64_t fill;        // table rows [0, fill) are zeroed beside the sort (0 when accumulating)
+  int64_t zero_rows;   // rows of the others that a warp looks up and zeroes
 };
 
 inline Plan make_plan(int64_t R, int64_t Vt, int64_t D, bool f32) {
@@ -61,6 +62,10 @@ inline int64_t fill_rows(const Plan& p, int64_t row_bytes) {
   const int64_t bytes = p.R <= kSmallRows ? 64000000 : 48000000 * p.passes;
   return std::min(p.Vt, bytes / row_bytes);
 }
+
+// Rows per warp of those left: 32 share a look into the keys, but few rows are spread over
+// more warps (16 MB in rows of 4 KB: 18 us by 125 warps).
+inline int64_t zero_rows(int64_t left) { return left >= 32 * 148 * 16 ? 32 : left >= 8 * 148 * 16 ? 8 : 2; }
 
 // CTAs that zero those rows: one per 16 KB of each of `parts` kernels, up to `most`.
 inline int fill_ctas(const Plan& p, int64_t row_bytes, int parts, int most) {

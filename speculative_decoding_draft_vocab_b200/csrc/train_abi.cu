@@ -157,6 +157,7 @@ dspark_status_t dspark_embed_bwd(const dspark_embed_problem_t* prob, const void*
   a.accumulate = accumulate ? 1 : 0;
   a.plan = embed_plan(prob);
   if (!accumulate) a.plan.fill = embed::fill_rows(a.plan, prob->D * elem_size(dtable_dtype));
+  a.plan.zero_rows = embed::zero_rows(prob->Vt - a.plan.fill);
   a.ws = embed::view(ws, a.plan);
   return cuda_status(embed::launch_bwd(a, reinterpret_cast<cudaStream_t>(stream)));
 }
