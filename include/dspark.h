@@ -339,9 +339,9 @@ DSPARK_API dspark_status_t dspark_tp_heads_bwd(const dspark_problem_t* prob, con
  * over the whole vocabulary, from the hidden rows and the head, with its gradients.  The
  * caller has no logits: the forward leaves one logsumexp per row, the backward forms dL/dz
  * again, one piece of the vocabulary at a time.  Only where all the FP32 logits take at most
- * 320 MiB, and the forward's workspace has room for a backward, do they stay there and spare
- * the backward a product.  (The CE term of dspark_loss_fwd, for callers that have hidden
- * rows instead of logits.)
+ * 320 MiB, and the forward's ws_bytes has room for a backward, do they stay there and spare
+ * the backward a product; the workspace says which, and a backward goes by that.  (The CE
+ * term of dspark_loss_fwd, for callers that have hidden rows instead of logits.)
  *   lse_r = logsumexp(z_r),   CE_r = lse_r - z_r[target_r]
  *   loss  = sum_r w_r * (CE_r + z_alpha * lse_r^2)          (unnormalised numerator)
  *   dz_r  = g * w_r * (softmax(z_r) * (1 + 2 z_alpha lse_r) - onehot(target_r))
@@ -402,7 +402,10 @@ typedef struct {
 DSPARK_API size_t dspark_lce_workspace_size(const dspark_lce_problem_t* prob, const dspark_lce_grads_t* grads);
 
 /* Forward.  `ws` 256-byte aligned, dspark_lce_workspace_size(prob, NULL) bytes, or as many
- * as the backward needs if one follows on the same workspace. */
+ * as the backward needs if one follows on the same workspace.  ws_bytes decides whether
+ * logits are kept: with the forward's own size none are written, also into a larger buffer
+ * (scoring in a workspace that a training step uses too); a backward that follows all the
+ * same forms them again. */
 DSPARK_API dspark_status_t dspark_lce_fwd(const dspark_lce_problem_t* prob, const dspark_lce_out_t* out, void* ws,
                                           size_t ws_bytes, dspark_stream_t stream);
 

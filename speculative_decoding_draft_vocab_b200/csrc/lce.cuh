@@ -29,7 +29,8 @@ struct WsLceHeader {
   int32_t n_valid;     // labelled rows
   uint32_t done;       // merge CTAs finished
   uint32_t redo;       // gathered forward: a row's exponentials left their range
-  uint32_t pad[60];
+  uint32_t kept;       // the forward left its logits in the workspace
+  uint32_t pad[59];
 };
 static_assert(sizeof(WsLceHeader) == 256, "header is one 256-byte line");
 
@@ -45,7 +46,7 @@ struct Plan {
   int64_t plane_rows;  // rows of the hidden gradient's partial sums, all planes together
   uint8_t ksplit[kMaxSplitTiles + 1];  // its K splits (planes) by the number of row tiles
   int64_t merge_blocks;
-  int keep;            // the logits stay in the workspace where it has room for a backward
+  int keep;            // the logits stay in the workspace if the forward was given room for a backward
   int gathered;        // the forward also gathers the hidden gradient (no head gradient follows)
 };
 
@@ -153,7 +154,8 @@ inline View view(void* base, const Plan& p) {
   return v;
 }
 
-// `keep`: the workspace holds the plan's kept logits.
+// `keep`: the workspace has room for the plan's kept logits.  The header says whether the
+// last forward kept them; the backward goes by that, whatever room it was given itself.
 cudaError_t launch_fwd(const dspark_lce_problem_t& p, const dspark_lce_out_t& out, const Plan& plan, const View& ws,
                        bool keep, cudaStream_t s);
 cudaError_t launch_bwd(const dspark_lce_problem_t& p, const dspark_lce_grads_t& g, const Plan& plan, const View& ws,

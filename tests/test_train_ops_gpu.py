@@ -693,3 +693,37 @@ def test_linear_ce_gathered_out_of_the_reference_range(T, R):
     bad = torch.isnan(call.lse_rows)
     assert bool(bad[4]) and int(bad.sum()) == 1
     assert not bool(torch.isnan(call.dhidden[torch.arange(R, device="cuda") != 4]).any())
+
+
+# --------------------------------------- a backward that forms the logits again
+def forward_alone(call):
+    """The forward with the workspace size that it needs by itself: it keeps no logits."""
+    import ctypes
+    from speculative_decoding_draft_vocab_b200 import abi
+    n = abi.dspark_lce_workspace_size(ctypes.byref(call.prob), None)
+    assert n < call.ws_len
+    s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    abi.check(abi.dspark_lce_fwd(ctypes.byref(call.prob), ctypes.byref(call.out), call.ws_ptr, n, s), "dspark_lce_fwd")
+    call._ran = True
+
+
+@pytest.mark.parametrize("R,V,H", [(100, 1003, 72), (300, 5000, 136)])
+def test_linear_ce_backward_goes_by_what_its_forward_kept(T, R, V, H):
+    """A forward that was given no room for the logits, on a workspace that holds those of an
+    earlier forward: the backward must not take these for its own."""
+    h, w, t, a = lce_inputs(R, V, H, 9, seed=30)
+    call = T.LinearCE(h, w, t, row_weight=a)
+    call.forward()
+    call.backward()
+    lce_compare(call, O.linear_ce(h, w, t, a), H, V)
+    h2, _, t2, _ = lce_inputs(R, V, H, 5, seed=31)
+    h.copy_(h2)
+    t.copy_(t2)
+    ref = O.linear_ce(h, w, t, a)
+    forward_alone(call)
+    call.backward()
+    assert call.check_status() == 0
+    lce_compare(call, ref, H, V)
+    call.forward()  # and kept again
+    call.backward()
+    lce_compare(call, ref, H, V)
