@@ -727,3 +727,40 @@ def test_linear_ce_backward_goes_by_what_its_forward_kept(T, R, V, H):
     call.forward()  # and kept again
     call.backward()
     lce_compare(call, ref, H, V)
+
+
+@pytest.mark.parametrize("R,V,H,ignored", [(64, 1500, 4096, 3), (100, 3001, 328, 9), (129, 2000, 1000, 0),
+                                           (300, 5003, 1000, 120), (700, 4100, 4096, 50)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_linear_ce_forms_its_logits_again(T, R, V, H, ignored, dtype):
+    """What larger batches do, at small ones: dz from the product again, over hidden sizes of
+    several K chunks and segments, with a z-loss, strides and a scale."""
+    h, w, t, a = lce_inputs(R, V, H, ignored, seed=R + H, hidden_pad=8, weight_pad=16)
+    call = T.LinearCE(h, w, t, row_weight=a, z_alpha=1e-3, dweight_dtype=dtype)
+    call.grad_scale.fill_(-1.25)
+    forward_alone(call)
+    call.backward()
+    assert call.check_status() == 0
+    ref = O.linear_ce(h, w, t, a, z_alpha=1e-3, grad_scale=-1.25)
+    lce_compare(call, ref, H, V)
+    first = [call.dhidden.clone(), call.dweight.clone()]
+    call.backward()
+    assert torch.equal(first[0], call.dhidden) and torch.equal(first[1], call.dweight)
+    if dtype == torch.float32:  # added to what is there
+        base = torch.randn(V, H, device="cuda")
+        more = T.LinearCE(h, w, t, row_weight=a, z_alpha=1e-3, dhidden=False, dweight=base.clone(), accumulate=True)
+        more.grad_scale.fill_(-1.25)
+        forward_alone(more)
+        more.backward()
+        lce_compare(more, ref, H, V, base=base)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_linear_ce_head_gradient_alone_in_pieces(T, dtype):
+    R, V, H = 8192, 20011, 72
+    h, w, t, a = lce_inputs(R, V, H, 700, seed=32)
+    call = T.LinearCE(h, w, t, row_weight=a, dhidden=False, dweight_dtype=dtype)
+    call.forward()
+    call.backward()
+    assert call.check_status() == 0
+    lce_compare(call, O.linear_ce(h, w, t, a), H, V)
