@@ -485,11 +485,13 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   constexpr bool B_MN = EPI == kDh || A_MN;
   constexpr int STAGES = stages<CG>(EPI);
   // The tensor cores' FP32 accumulation rounds towards zero: over K = 4096 the logits come
-  // out 2.2e-6 short (relative), over K = 512 3e-7.  The forward hands over its accumulator
-  // every 512 values of K and the epilogue adds the segments in registers, rounding to
-  // nearest; the other products are rounded to bf16 right after, where it does not show.
-  constexpr bool SEGMENTED = EPI == kFwd || EPI == kFwdKeep || EPI == kGather;
-  constexpr int SEG = SEGMENTED ? 512 / BK : 1 << 29;
+  // out 2.2e-6 short (relative), over K = 512 3e-7, and sums over K rows or columns about
+  // K 2e-9.  So no accumulator runs over a whole K range: it is handed over in segments, which
+  // the epilogue adds in registers, rounding to nearest.  The forward's logits, whose errors
+  // the exponentials magnify, take segments of 512 values; dz, the planes and dweight, which
+  // pass through bf16 factors of 2^-9, take 4096.
+  constexpr bool LOGITS = EPI == kFwd || EPI == kFwdKeep || EPI == kGather;
+  constexpr int SEG = (LOGITS ? 512 : 4096) / BK;
   constexpr uint32_t SA = kBM * BK * 2, SS = stage_bytes<CG>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -639,31 +641,38 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                           ::"r"(dsmem_map(acce0 + 8 * b, 0)) : "memory");
       }
     };
+    // Adds the accumulator of segment `tl` to this warp's share.
+    auto add_segment = [&](int tl, float (&z)[128]) {
+      const int b = tl & 1;
+      if (!mbar_wait_bounded(accf0 + 8 * b, uint32_t(tl >> 1) & 1u)) timed_out = true;
+      tc::fence_after_sync();
+      const uint32_t taddr = tmem_base + lanes + uint32_t(b * 256 + sh.c0);
+      constexpr int N = LOGITS ? 16 : 4;  // columns at a time (8 spill in some of the gradient products)
+#pragma unroll
+      for (int c = 0; c < 128; c += N) {
+        float v[N];
+        __syncwarp();
+        if constexpr (N == 16) {
+          tmem_ld16(taddr + uint32_t(c), v);
+          tmem_wait16(v);
+        } else {
+          tm::ld<N>(taddr + uint32_t(c), v);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[c + i] += v[i];
+      }
+      release(b);
+    };
     int tl = 0;
     for (int w = tile0; w < W; w += tiles_step) {
       const Item t = decode(wk, w, me, kch, ks);
       sh.m0 = (t.mt * CG + int(rank)) * kBM + q * 32, sh.n0 = t.nt * bn;
       sh.nt = t.nt, sh.plane0 = t.s * me * kBM * CG, sh.empty = t.kc0 == t.kc1;
-      if constexpr (SEGMENTED) {
+      if constexpr (LOGITS) {
         float z[128];
 #pragma unroll
         for (int i = 0; i < 128; ++i) z[i] = 0.f;
-        for (int kc = t.kc0; kc < t.kc1; kc += SEG, ++tl) {
-          const int b = tl & 1;
-          if (!mbar_wait_bounded(accf0 + 8 * b, uint32_t(tl >> 1) & 1u)) timed_out = true;
-          tc::fence_after_sync();
-          const uint32_t taddr = tmem_base + lanes + uint32_t(b * 256 + sh.c0);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            float v[16];
-            __syncwarp();
-            tmem_ld16(taddr + uint32_t(16 * c), v);
-            tmem_wait16(v);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) z[16 * c + i] += v[i];
-          }
-          release(b);
-        }
+        for (int kc = t.kc0; kc < t.kc1; kc += SEG, ++tl) add_segment(tl, z);
         if constexpr (EPI == kGather) gather_finish(ea, tmO, sh, z);
         else fwd_finish(ea, sh, z);
         if constexpr (EPI == kFwdKeep) f32_finish<EPI>(ea, tmO, sh, z);
@@ -675,6 +684,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         float z[128];
         tmem_ld128(tmem_base + lanes + uint32_t(b * 256 + sh.c0), z);
         release(b);
+        for (int kc = t.kc0 + SEG; kc < t.kc1; kc += SEG) add_segment(++tl, z);
         if constexpr (EPI == kDz) dz_finish(ea, tmO, sh, z);
         else if constexpr (EPI == kDwBf16) bf16_finish(ea, tmO, sh, z);
         else f32_finish<EPI>(ea, tmO, sh, z);

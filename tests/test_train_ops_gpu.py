@@ -764,3 +764,45 @@ def test_linear_ce_head_gradient_alone_in_pieces(T, dtype):
     call.backward()
     assert call.check_status() == 0
     lce_compare(call, O.linear_ce(h, w, t, a), H, V)
+
+
+def test_linear_ce_sums_over_many_rows_do_not_fall_short(T):
+    """An FP32 head gradient over 100003 rows.  Logits of zero over four columns: dz is 1/4
+    exactly where there is no label, so dz's rounding takes no part and the sums of positive
+    terms stand alone.  Accumulators round towards zero within segments of 4096 rows (at most
+    2^-23 of the sum at each of 4096 / 16 steps, and 2 more for the product), the segments are
+    added to nearest."""
+    R, V, H = 100003, 4, 64
+    g = torch.Generator(device="cuda").manual_seed(33)
+    h = (torch.rand(R, H, generator=g, device="cuda") + 1.0).to(torch.bfloat16)
+    w = torch.zeros(V, H, dtype=torch.bfloat16, device="cuda")
+    t = torch.zeros(R, dtype=torch.int64, device="cuda")
+    call = T.LinearCE(h, w, t, dhidden=False, dweight_dtype=torch.float32)
+    call.forward()
+    call.backward()
+    assert call.check_status() == 0
+    total = h.double().sum(0)
+    want = torch.stack([-0.75 * total] + 3 * [0.25 * total])
+    bound = (4096 / 16 + 2) * 2.0 ** -23 + (R / 4096 + 2) * 2.0 ** -24
+    assert bool(((call.dweight.double() - want).abs() <= bound * want.abs()).all())
+
+
+def test_linear_ce_long_hidden_rows(T):
+    """dz from the product again over a hidden size of 2^18, all terms positive: its logits may
+    be short by the rounding of a segment of 4096 and of the segments' sum, not by that of the
+    whole length (bounds of the head of this file, with the segments' E')."""
+    R, V, H = 20, 40, 1 << 18
+    g = torch.Generator(device="cuda").manual_seed(34)
+    h = ((torch.rand(R, H, generator=g, device="cuda") + 0.5) * 0.0276).to(torch.bfloat16)
+    w = ((torch.rand(V, H, generator=g, device="cuda") + 0.5) * 0.0276).to(torch.bfloat16)
+    t = torch.arange(R, device="cuda")
+    call = T.LinearCE(h, w, t)
+    forward_alone(call)
+    call.backward()
+    assert call.check_status() == 0
+    ref = O.linear_ce(h, w, t)
+    E = (32 + H / 512 + 2) * 2.0 ** -23 * ref["reach"]
+    P = 2 * ((4096 / 16 + H / 4096 + 2) * 2.0 ** -23 * ref["reach"] + E) + 2.0 ** -20
+    assert bool(((call.lse_rows.double() - ref["lse_rows"]).abs() <= E + 2.0 ** -20 + 2.0 ** -22 * ref["lse_rows"]).all())
+    tol = P * ref["dw_pmag"] + (U16 + 4 * 2.0 ** -23) * ref["dw_mag"] + U16 * ref["dweight"].abs()
+    assert bool(((call.dweight.double() - ref["dweight"]).abs() <= tol).all())
