@@ -197,6 +197,7 @@ struct EpiArgs {
   float z_alpha;
   const float* grad_scale;
   int32_t add;               // dh: add to the planes; dw: add to dweight
+  int32_t watch;             // dh of a gathered forward: a plane that nears FP32's range asks for the other way
   int32_t when;              // kIfRedo: only where a gathered forward has to be done the other way;
                              // kIfNotKept: only where the forward did not keep its logits
 };
@@ -398,9 +399,9 @@ __device__ __forceinline__ void dz_finish(const EpiArgs& a, const CUtensorMap& o
 // Gathered forward: the row's exponentials relative to its reference, as bf16 for the product
 // with the head and summed in FP32; the logit at the label.  The label's column is left out
 // of the product: its factor in the gradient is p - 1, which for a row that is nearly right
-// is far below the rounding of p.  A logit 100 octaves above the
-// reference (69 above the largest of the sampled columns) would leave bf16's and FP32's range
-// in the sums: it is reported, and the call goes the other way.
+// is far below the rounding of p.  A logit 96 octaves above the reference (66 above the
+// largest of the sampled columns) is reported, and the call goes the other way: below that
+// the sum of 2^30 exponentials stays in FP32's range.
 __device__ __forceinline__ void gather_finish(const EpiArgs& a, const CUtensorMap& out, Share& sh, float (&z)[128]) {
   if (sh.m0 >= a.rows) return;  // the whole warp
   const int row = sh.m0 + sh.lane;
@@ -442,7 +443,7 @@ __device__ __forceinline__ void gather_finish(const EpiArgs& a, const CUtensorMa
     store_box(sh, out, o, n0 + c, sh.m0, 0, staging_tiles(kGather));
   }
   if (!live) return;
-  if (top > 100.f) a.ws.hdr->redo = 1;  // every writer writes the same
+  if (top > kGatherRange) a.ws.hdr->redo = 1;  // every writer writes the same
   a.ws.part[size_t(2 * (a.col0 / kBN + sh.nt) + sh.half) * a.plan.Rp + row] =
       make_float2(ref, (s4[0] + s4[1]) + (s4[2] + s4[3]));
 }
@@ -452,6 +453,16 @@ __device__ __forceinline__ void gather_finish(const EpiArgs& a, const CUtensorMa
 template <int EPI>
 __device__ __forceinline__ void f32_finish(const EpiArgs& a, const CUtensorMap& out, Share& sh, const float (&z)[128]) {
   if (sh.m0 >= (EPI == kDh || EPI == kFwdKeep ? sh.n_valid : a.rows) || (sh.empty && a.add)) return;
+  if constexpr (EPI == kDh) {
+    // 32 splits of at most 2^22 pieces of the vocabulary, each below this, add up to less than
+    // 2^127 (columns past the hidden size are zeros)
+    if (a.watch && !sh.empty && sh.m0 + sh.lane < sh.n_valid) {
+      bool in = true;
+#pragma unroll
+      for (int i = 0; i < 128; ++i) in = in && (i >= sh.cols || fabsf(z[i]) < 1e30f);
+      if (!in) a.ws.hdr->redo = 1;  // every writer writes the same
+    }
+  }
 #pragma unroll
   for (int c = 0; c < 128; c += 32) {
     if (c >= sh.cols || sh.n0 + sh.c0 + c >= a.n_cols) break;
@@ -988,6 +999,7 @@ cudaError_t launch_pieces(const dspark_lce_problem_t& p, const dspark_lce_grads_
     ea.col0 = int32_t(v0);
     ea.z_alpha = p.z_alpha;
     ea.grad_scale = g.grad_scale;
+    ea.watch = what == kGather;
     ea.when = what != kDz ? kAlways : pl.gathered ? kIfRedo : pl.keep ? kIfNotKept : kAlways;
     const Work wz = make_work(tiles(p.R, kBM * pl.cg), tiles(n, kBN), tiles(p.H, BK), 16, false, ws);
     // Of the product and dz_kernel one returns at once: only the device knows what the forward

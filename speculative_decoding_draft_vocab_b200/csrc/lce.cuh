@@ -20,6 +20,8 @@ constexpr size_t kPlaneBytes = size_t(96) << 20;     // bound on split planes (t
 constexpr size_t kKeepBytes = size_t(320) << 20;
 // A gathered forward takes the reference of a row's exponentials from this many columns.
 constexpr int kSampleCols = 2048;
+// A logit more than this many octaves above a row's reference sends the call the other way.
+constexpr float kGatherRange = 96.f;
 // From this vocabulary on it pays: it saves one of three products and adds the sample.
 constexpr int64_t kGatherFrom = 16384;
 constexpr int kMergeRows = 32;                       // rows per CTA of the merge kernel
@@ -28,7 +30,7 @@ struct WsLceHeader {
   uint32_t status;     // device error bits
   int32_t n_valid;     // labelled rows
   uint32_t done;       // merge CTAs finished
-  uint32_t redo;       // gathered forward: a row's exponentials left their range
+  uint32_t redo;       // gathered forward: exponentials, or their products with the head, left their range
   uint32_t kept;       // the forward left its logits in the workspace
   uint32_t pad[59];
 };

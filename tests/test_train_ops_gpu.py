@@ -806,3 +806,28 @@ def test_linear_ce_long_hidden_rows(T):
     assert bool(((call.lse_rows.double() - ref["lse_rows"]).abs() <= E + 2.0 ** -20 + 2.0 ** -22 * ref["lse_rows"]).all())
     tol = P * ref["dw_pmag"] + (U16 + 4 * 2.0 ** -23) * ref["dw_mag"] + U16 * ref["dweight"].abs()
     assert bool(((call.dweight.double() - ref["dweight"]).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("R", [60, 200])
+@pytest.mark.parametrize("big", [10, 50])
+def test_linear_ce_gathered_with_a_large_head_column(T, R, big):
+    """A head column of 2^56 against hidden values of 2^-50, and a logit past the sampled
+    columns 80 octaves above them: 2^80 times 2^56 is beyond FP32, the gradient itself is not.
+    (With 2^16 it stays in range.)"""
+    V, H = 16500, 16
+    g = torch.Generator(device="cuda").manual_seed(35)
+    h = torch.randn(R, H, generator=g, device="cuda").to(torch.bfloat16)
+    w = (torch.randn(V, H, generator=g, device="cuda") * 0.5).to(torch.bfloat16)
+    h[:, 0] = 2.0 ** -big
+    w[:, 0] = 0.0
+    w[V - 3, 0] = 62.0 * 2.0 ** big
+    t = torch.arange(R, device="cuda") * 7 % V
+    t[3] = V - 3
+    call = T.LinearCE(h, w, t, dweight=False)
+    assert call.prob.hidden_grad_only == 1
+    for _ in range(2):  # the second forward begins anew
+        call.forward()
+        call.backward()
+        assert call.check_status() == 0
+        assert bool(torch.isfinite(call.dhidden).all())
+        lce_compare(call, O.linear_ce(h, w, t), H, V)
