@@ -461,10 +461,12 @@ DSPARK_API dspark_status_t dspark_embed_bwd(const dspark_embed_problem_t* prob, 
 /*
  * Global gradient norm and clipping over many tensors (the gradients above, say).
  *   sumsq = sum over all tensors of x^2,  norm = sqrt(sumsq)
- *   coef  = min(1, max_norm / (norm + 1e-6)), or 1 where the norm is not finite
+ *   coef  = min(1, max_norm / (norm + 1e-6)), or 1 where sumsq is not finite
  *   dst_t = coef * src_t, rounded once to the tensor's type
- * A norm that is not finite leaves the values as they are (the caller sees the norm and
- * skips its step).  Sums are FP64 in a fixed order: two runs give the same bits.
+ * A NaN or an infinity among the values leaves them as they are (the caller sees the norm and
+ * skips its step).  Finite values are clipped also where their norm is past FP32's range (and
+ * reported as infinity) or coef below it.  Sums are FP64 in a fixed order: two runs give the
+ * same bits.
  *
  * `tensors` is a HOST array of `count` descriptors, read during the call.  src and dst are
  * device pointers of n contiguous elements, aligned to their element; n may be 0; dst may

@@ -200,6 +200,15 @@ __device__ void chunk_scale(const void* src, void* dst, int64_t n, float coef) {
   }
 }
 
+// The same with the product taken in FP64: a coefficient below FP32's normal range (a norm of
+// 1e38 and more, a tiny max_norm) has lost its bits there, though the product need not be small.
+// No call for speed here: one element at a time.
+template <bool BF16>
+__device__ void chunk_scale_wide(const void* src, void* dst, int64_t n, double coef) {
+#pragma unroll 1
+  for (int64_t i = threadIdx.x; i < n; i += kThreads) store1<BF16>(dst, i, float(double(load1<BF16>(src, i)) * coef));
+}
+
 template <int N>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Batch<N> b, const double* sumsq,
                                                          const double* part, int64_t n_part, float max_norm,
@@ -208,9 +217,17 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
   pdl_trigger();
   __shared__ double sh[kThreads / 32];
   const double ss = sumsq ? *sumsq : total_of(part, n_part, sh);
-  const float norm = float(sqrt(ss));
-  const bool finite = isfinite(norm);
-  const float coef = finite ? fminf(max_norm / (norm + 1e-6f), 1.f) : 1.f;
+  const double root = sqrt(ss);
+  const float norm = float(root);
+  // In FP32 (an FP64 division here costs calls of small tensors 2.6 of 13.6 us) where norm and
+  // coefficient are in its range, else in FP64.
+  float coef = isfinite(norm) ? fminf(max_norm / (norm + 1e-6f), 1.f) : 1.f;
+  const bool wide = isfinite(root) && (!isfinite(norm) || coef < 0x1p-126f);
+  double coef_wide = 1.0;
+  if (wide) {
+    coef_wide = fmin(double(max_norm) / (root + 1e-6), 1.0);
+    coef = float(coef_wide);
+  }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     if (status) *status = 0u;
     if (norm_out) *norm_out = norm;
@@ -220,10 +237,10 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
     const Tensor& t = b.t[find(b, c)];
     if (coef == 1.f && t.src == t.dst) continue;  // in place and unchanged
     const int64_t at = int64_t(c - t.chunk0) * kChunk, n = min(kChunk, t.n - at);
-    if (t.bf16)
-      chunk_scale<true>(static_cast<const uint16_t*>(t.src) + at, static_cast<uint16_t*>(t.dst) + at, n, coef);
-    else
-      chunk_scale<false>(static_cast<const float*>(t.src) + at, static_cast<float*>(t.dst) + at, n, coef);
+    const uint8_t* src = static_cast<const uint8_t*>(t.src) + at * (t.bf16 ? 2 : 4);
+    uint8_t* dst = static_cast<uint8_t*>(t.dst) + at * (t.bf16 ? 2 : 4);
+    if (wide) t.bf16 ? chunk_scale_wide<true>(src, dst, n, coef_wide) : chunk_scale_wide<false>(src, dst, n, coef_wide);
+    else t.bf16 ? chunk_scale<true>(src, dst, n, coef) : chunk_scale<false>(src, dst, n, coef);
   }
 }
 

@@ -831,3 +831,22 @@ def test_linear_ce_gathered_with_a_large_head_column(T, R, big):
         assert call.check_status() == 0
         assert bool(torch.isfinite(call.dhidden).all())
         lce_compare(call, O.linear_ce(h, w, t), H, V)
+
+
+# ----------------------------------------------------- norms past FP32's range
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,max_norm", [(2, 1.0), (50001, 1.0), (50001, 1e-30)])
+def test_clip_by_a_norm_past_fp32(T, dtype, n, max_norm):
+    """Finite values whose norm FP32 does not hold are clipped all the same; the coefficient
+    may be far below FP32's range when the clipped values are not."""
+    g = torch.full((n,), 3e38, device="cuda").to(dtype)
+    g[::2] *= -1
+    norm, coef, want = O.clip([g], max_norm)
+    assert norm > torch.finfo(torch.float32).max and coef < torch.finfo(torch.float32).tiny
+    for out in (torch.zeros(n + 1, dtype=dtype, device="cuda")[1:], None):  # other alignment, in place
+        call = T.GradClip([g], max_norm, outs=None if out is None else [out])
+        call.launch()
+        assert call.check_status() == 0 and float(call.norm) == float("inf")
+        assert abs(float(call.coef) - coef) <= 2.0 ** -150 + 2.0 ** -20 * coef
+        # the sum of squares in FP64 and the product's and the type's roundings
+        assert bool(((call.outs[0].double() - want[0]).abs() <= (2.0 ** -20 + 1.01 * _u(dtype)) * want[0].abs()).all())
