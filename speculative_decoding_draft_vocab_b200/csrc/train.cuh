@@ -129,7 +129,9 @@ constexpr int kThreads = 256;
 constexpr int64_t kChunk = 8192;   // elements a CTA takes at a time
 
 inline int64_t launches(int64_t count) { return (count + kMaxTensors - 1) / kMaxTensors; }
-// workspace: 256-byte header, then one FP64 partial sum per CTA and launch
+// workspace: 256-byte header (status word, the total at byte 8), then one FP64 partial sum per
+// CTA and launch
+inline double* total_of_call(void* ws) { return reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + 8); }
 inline size_t ws_bytes(int64_t count) { return align256(256 + sizeof(double) * size_t(launches(count)) * kGrid); }
 
 cudaError_t launch_sumsq(const dspark_tensor_t* t, int64_t count, void* ws, cudaStream_t s, int64_t* partials);

@@ -196,9 +196,17 @@ dspark_status_t dspark_grad_clip(const dspark_tensor_t* tensors, int64_t count, 
   if ((st = check_ws(ws, ws_bytes, clip::ws_bytes(count))) != DSPARK_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int64_t n = 0;
-  const cudaError_t e = clip::launch_sumsq(tensors, count, ws, s, &n);
+  cudaError_t e = clip::launch_sumsq(tensors, count, ws, s, &n);
   if (e != cudaSuccess) return cuda_status(e);
-  return cuda_status(clip::launch_scale(tensors, count, nullptr, n, max_norm, norm, coef, ws, s));
+  // One launch's partial sums are few: every CTA of the scaling adds them up for itself.  Those
+  // of several are added up once (or each CTA of each launch would read all of them: 20000
+  // tensors of 9000 bf16 elements 668 against 429 us).
+  double* total = nullptr;
+  if (clip::launches(count) > 1) {
+    total = clip::total_of_call(ws);
+    if ((e = clip::launch_total(ws, n, total, s)) != cudaSuccess) return cuda_status(e);
+  }
+  return cuda_status(clip::launch_scale(tensors, count, total, n, max_norm, norm, coef, ws, s));
 }
 
 }  // extern "C"

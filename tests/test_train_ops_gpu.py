@@ -850,3 +850,32 @@ def test_clip_by_a_norm_past_fp32(T, dtype, n, max_norm):
         assert abs(float(call.coef) - coef) <= 2.0 ** -150 + 2.0 ** -20 * coef
         # the sum of squares in FP64 and the product's and the type's roundings
         assert bool(((call.outs[0].double() - want[0]).abs() <= (2.0 ** -20 + 1.01 * _u(dtype)) * want[0].abs()).all())
+
+
+def test_clip_of_many_launches_in_one_call_and_in_two_steps(T):
+    """3000 tensors, more than one launch describes: one call adds the launches' partial sums up
+    once, in the order the two steps do, and gives the same bits; replayed too."""
+    import ctypes
+    from speculative_decoding_draft_vocab_b200 import abi
+    _, grads = _flat([9001, 0, 17] * 1000, torch.bfloat16, 1, seed=40)
+    outs = [torch.empty_like(g) for g in grads]
+    call = T.GradClip(grads, 2.0, outs=outs)
+    call.launch()
+    norm, coef, want = O.clip(grads, 2.0)
+    assert abs(float(call.norm) - norm) <= 2.0 ** -21 * norm and call.check_status() == 0
+    first = [call.norm.clone(), call.coef.clone(), torch.cat(outs)]
+    s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    abi.check(abi.dspark_grad_sumsq(call.tensors, call.count, call.sumsq.data_ptr(), call.ws_ptr, call.ws_len, s), "sumsq")
+    abi.check(abi.dspark_grad_scale(call.tensors, call.count, call.sumsq.data_ptr(), 2.0, call.norm.data_ptr(),
+                                    call.coef.data_ptr(), call.ws_ptr, call.ws_len, s), "scale")
+    assert all(torch.equal(x, y) for x, y in zip(first, (call.norm, call.coef, torch.cat(outs))))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call.launch()
+    for g in grads[:2000]:
+        g.mul_(4.0)
+    graph.replay()
+    norm, coef, want = O.clip(grads, 2.0)
+    assert abs(float(call.norm) - norm) <= 2.0 ** -21 * norm
+    got = torch.cat(outs).double()
+    assert bool(((got - torch.cat(want)).abs() <= (2.0 ** -20 + 1.01 * U16) * torch.cat(want).abs()).all())
