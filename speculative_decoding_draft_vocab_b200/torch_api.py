@@ -610,9 +610,15 @@ class GradClip(_DeviceCall):
     ``group`` dspark_grad_sumsq, an all-reduce of its FP64 sum over that process group, and
     dspark_grad_scale).  ``grads`` are contiguous bf16 or fp32 tensors; the clipped values
     go to ``outs`` (same types and sizes) or back into ``grads``.  launch() writes ``norm``
-    and ``coef``."""
+    and ``coef``.
 
-    def __init__(self, grads, max_norm: float, outs=None, group=None):
+    Over a group every rank's tensors count, as shards of one gradient do.  Those of which
+    each rank holds the same copy (a TPRank's dW1, dconf_w and dconf_b beside its shard of
+    dW2) have to be named in ``replicated`` as well: they count once, by the copy of the
+    group's first rank, and each rank clips its own.  Every rank then gets the same norm and
+    coefficient."""
+
+    def __init__(self, grads, max_norm: float, outs=None, group=None, replicated=()):
         grads = list(grads)
         outs = grads if outs is None else list(outs)
         if not grads or len(outs) != len(grads):
@@ -632,6 +638,17 @@ class GradClip(_DeviceCall):
             arr[i] = abi.dspark_tensor_t(g.data_ptr(), o.data_ptr(), g.numel(), _ABI_DTYPE[g.dtype])
         self.tensors, self.count, self.max_norm, self.group = arr, len(grads), float(max_norm), group
         self.grads, self.outs = grads, outs
+        copies = {id(t) for t in replicated}
+        if copies - {id(g) for g in grads}:
+            raise ValueError("replicated must name tensors of grads")
+        self._summed = (arr, len(grads))  # what this rank adds to the group's sum
+        if group is not None and copies:
+            import torch.distributed as dist
+            if dist.get_rank(group) != 0:
+                own = [i for i, g in enumerate(grads) if id(g) not in copies]
+                # (a tensor without elements where every one is a copy)
+                rows = [arr[i] for i in own] or [abi.dspark_tensor_t(None, None, 0, abi.DSPARK_F32)]
+                self._summed = ((abi.dspark_tensor_t * len(rows))(*rows), len(rows))
         self.norm = torch.zeros(1, dtype=torch.float32, device=self.device)
         self.coef = torch.ones(1, dtype=torch.float32, device=self.device)
         self.sumsq = torch.zeros(1, dtype=torch.float64, device=self.device)
@@ -645,8 +662,8 @@ class GradClip(_DeviceCall):
         import torch.distributed as dist
         if stream is not None:
             raise ValueError("with a process group the call runs on the current stream")
-        self._run(abi.dspark_grad_sumsq, "dspark_grad_sumsq", None, self.tensors, self.count, _ptr(self.sumsq),
-                  self.ws_ptr, self.ws_len)
+        self._run(abi.dspark_grad_sumsq, "dspark_grad_sumsq", None, *self._summed, _ptr(self.sumsq), self.ws_ptr,
+                  self.ws_len)
         dist.all_reduce(self.sumsq, op=dist.ReduceOp.SUM, group=self.group)
         self._run(abi.dspark_grad_scale, "dspark_grad_scale", None, self.tensors, self.count, _ptr(self.sumsq),
                   *self._tail)

@@ -879,3 +879,37 @@ def test_clip_of_many_launches_in_one_call_and_in_two_steps(T):
     assert abs(float(call.norm) - norm) <= 2.0 ** -21 * norm
     got = torch.cat(outs).double()
     assert bool(((got - torch.cat(want)).abs() <= (2.0 ** -20 + 1.01 * U16) * torch.cat(want).abs()).all())
+
+
+@pytest.mark.parametrize("shard", [True, False])
+def test_clip_counts_replicated_gradients_once(T, monkeypatch, shard):
+    """A vocabulary-parallel rank's gradients: its shard of dW2 beside its copies of dW1,
+    dconf_w and dconf_b.  Both ranks of a group of two get the norm of the whole gradient, in
+    which the copies count once (the collective is a stand-in that adds the other rank's sum)."""
+    import torch.distributed as dist
+    from speculative_decoding_draft_vocab_b200.synthetic import make_inputs
+    inp = make_inputs("recipe_heads", device="cuda", B=1, N=3, K=7, V=2048, hidden=256, rank=64, seed=4)
+    ranks = T.tp_group_emulated(inp, 2)
+    torch.cuda.synchronize()
+    sharded, copies = [], []
+    for r in ranks:
+        sharded.append([r.dW2[r.col0:r.col0 + r.width]] if shard else [])
+        copies.append([r.dW1, r.dconf_w, r.dconf_b])
+    sums = [sum(float(t.double().pow(2).sum()) for t in ts) for ts in (sharded[0] + copies[0], sharded[1])]
+    norm, coef, _ = O.clip(sharded[0] + sharded[1] + copies[0], 0.05)
+    assert norm > 0.05
+    calls = []
+    for k in range(2):
+        monkeypatch.setattr(dist, "get_rank", lambda group=None, k=k: k)
+        monkeypatch.setattr(dist, "all_reduce", lambda x, op=None, group=None, k=k: x.add_(sums[1 - k]))
+        grads = copies[k][:1] + sharded[k] + copies[k][1:]
+        call = T.GradClip(grads, 0.05, outs=[torch.empty_like(g) for g in grads], group="tp", replicated=copies[k])
+        call.launch()
+        assert call.check_status() == 0
+        # FP64 sums of squares each right to 2^-22, one square root and three FP32 roundings
+        assert abs(float(call.norm) - norm) <= 2.0 ** -21 * norm and abs(float(call.coef) - coef) <= 2.0 ** -20 * coef
+        for g, o in zip(grads, call.outs):
+            assert bool(((o.double() - g.double() * coef).abs() <= 2.0 ** -19 * (g.double() * coef).abs()).all())
+        calls.append(call)
+    with pytest.raises(ValueError, match="replicated"):
+        T.GradClip([ranks[0].dW1], 1.0, group="tp", replicated=[ranks[0].dconf_b])
