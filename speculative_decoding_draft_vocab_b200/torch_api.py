@@ -609,8 +609,8 @@ class GradClip(_DeviceCall):
     """A prepared clipping of many gradients by their global norm (dspark_grad_clip; with
     ``group`` dspark_grad_sumsq, an all-reduce of its FP64 sum over that process group, and
     dspark_grad_scale).  ``grads`` are contiguous bf16 or fp32 tensors; the clipped values
-    go to ``outs`` (same types and sizes) or back into ``grads``.  launch() writes ``norm``
-    and ``coef``.
+    go to ``outs`` (same types and sizes) or back into ``grads``.  No two tensors share
+    memory, but for an outs[i] that is grads[i].  launch() writes ``norm`` and ``coef``.
 
     Over a group every rank's tensors count, as shards of one gradient do.  Those of which
     each rank holds the same copy (a TPRank's dW1, dconf_w and dconf_b beside its shard of
@@ -636,6 +636,11 @@ class GradClip(_DeviceCall):
                 raise ValueError(f"grads[{i}] is listed twice")
             seen.add(g.data_ptr())
             arr[i] = abi.dspark_tensor_t(g.data_ptr(), o.data_ptr(), g.numel(), _ABI_DTYPE[g.dtype])
+        # what is read and what is written elsewhere: no two of them may share memory
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                       for t in grads + [o for g, o in zip(grads, outs) if o.data_ptr() != g.data_ptr()] if t.numel())
+        if any(end > start for (_, end), (start, _) in zip(spans, spans[1:])):
+            raise ValueError("grads and outs must not overlap (outs[i] may be grads[i])")
         self.tensors, self.count, self.max_norm, self.group = arr, len(grads), float(max_norm), group
         self.grads, self.outs = grads, outs
         copies = {id(t) for t in replicated}

@@ -913,3 +913,18 @@ def test_clip_counts_replicated_gradients_once(T, monkeypatch, shard):
         calls.append(call)
     with pytest.raises(ValueError, match="replicated"):
         T.GradClip([ranks[0].dW1], 1.0, group="tp", replicated=[ranks[0].dconf_b])
+
+
+def test_clip_refuses_tensors_that_share_memory(T):
+    """A part listed beside the whole, one output for two gradients, an output on another's
+    gradient: each would be scaled twice or read half written."""
+    buf, more = torch.randn(100, device="cuda"), torch.empty(100, device="cuda")
+    a, b, c = buf[:40], buf[40:], buf[30:60]
+    T.GradClip([a, b], 1.0).launch()
+    T.GradClip([a, b], 1.0, outs=[a, more[:60]]).launch()
+    T.GradClip([a, buf[40:40], b], 1.0, outs=[more[:40], more[10:10], more[40:]]).launch()
+    for grads, outs in (([a, b, c], None), ([buf, a], None), ([a, buf[40:80]], [more[:40], more[:40]]),
+                        ([a, buf[40:80]], [more[:40], more[39:79]]), ([a, buf[40:80]], [buf[40:80], a]),
+                        ([a], [buf[8:48]])):
+        with pytest.raises(ValueError, match="overlap|listed twice"):
+            T.GradClip(grads, 1.0, outs=outs)
