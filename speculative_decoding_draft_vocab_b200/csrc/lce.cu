@@ -39,6 +39,7 @@ namespace {
 using tc::BK;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr uint64_t kDrainNs = 1000000;
 
 // ------------------------------------------------------------------ prep
 // Each CTA takes a contiguous run of rows, counts the labelled rows before it (the labels
@@ -573,13 +574,16 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     // operands that the kernels before wrote by ordinary stores (the gathered rows, dz)
     asm volatile("fence.proxy.async.global;" ::: "memory");
     int it = 0;
-    for (int w = tile0; w < W; w += tiles_step) {
+    for (int w = tile0; w < W && !timed_out; w += tiles_step) {
       const Item t = decode(wk, w, me, kch, ks);
       const int am = (t.mt * CG + int(rank)) * kBM, bn0 = t.nt * bn + int(rank) * bnc;
       for (int kc = t.kc0; kc < t.kc1; ++kc, ++it) {
         const int st = it % STAGES;
         const uint32_t round = uint32_t(it / STAGES);
-        if (!mbar_wait_bounded(empty0 + 8 * st, (round & 1u) ^ 1u)) timed_out = true;
+        if (!mbar_wait_bounded(empty0 + 8 * st, (round & 1u) ^ 1u)) {
+          timed_out = true;
+          break;
+        }
         uint32_t fb = full0 + 8 * st;
         if (rank == 0) mbar_arrive_expect_tx(fb, tx);
         else fb = dsmem_map(fb, 0);
@@ -602,19 +606,21 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     // ---------------- MMA issuer
     const uint32_t idesc = tc::idesc_bf16(kBM * CG, bn, A_MN, B_MN);
     int it = 0, tl = 0;
-    for (int w = tile0; w < W; w += tiles_step) {
+    for (int w = tile0; w < W && !timed_out; w += tiles_step) {
       const Item t = decode(wk, w, me, kch, ks);
       int kc = t.kc0;
       do {  // one accumulator per segment (an empty K range still hands one over)
         const int b = tl & 1;
         if (!mbar_wait_bounded(acce0 + 8 * b, (uint32_t(tl >> 1) & 1u) ^ 1u)) timed_out = true;
         tc::fence_after_sync();
+        if (timed_out) break;
         const uint32_t d_tmem = tmem_base + uint32_t(b * 256);
         const int k1 = min(t.kc1, kc + SEG), kfirst = kc;
         for (; kc < k1; ++kc, ++it) {
           const int st = it % STAGES;
           if (!mbar_wait_bounded(full0 + 8 * st, uint32_t(it / STAGES) & 1u)) timed_out = true;
           tc::fence_after_sync();
+          if (timed_out) break;
           const uint32_t sa = smem_u32(smem + size_t(st) * SS), sb = sa + SA;
 #pragma unroll
           for (int k = 0; k < BK / 16; ++k) {
@@ -624,6 +630,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           }
           commit<CG>(empty0 + 8 * st);  // frees the stage once these MMAs have read it
         }
+        if (timed_out) break;
         commit<CG>(accf0 + 8 * b);  // accumulator ready
         ++tl;
       } while (kc < t.kc1);
@@ -652,11 +659,17 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                           ::"r"(dsmem_map(acce0 + 8 * b, 0)) : "memory");
       }
     };
+    // Waits for the accumulator of segment `tl`; the warp gives up as one.
+    auto arrived = [&](int tl) {
+      const bool ok = mbar_wait_bounded(accf0 + 8 * (tl & 1), uint32_t(tl >> 1) & 1u);
+      if (!__all_sync(0xffffffffu, ok)) timed_out = true;
+      tc::fence_after_sync();
+      return !timed_out;
+    };
     // Adds the accumulator of segment `tl` to this warp's share.
     auto add_segment = [&](int tl, float (&z)[128]) {
       const int b = tl & 1;
-      if (!mbar_wait_bounded(accf0 + 8 * b, uint32_t(tl >> 1) & 1u)) timed_out = true;
-      tc::fence_after_sync();
+      if (!arrived(tl)) return;
       const uint32_t taddr = tmem_base + lanes + uint32_t(b * 256 + sh.c0);
       constexpr int N = LOGITS ? 16 : 4;  // columns at a time (8 spill in some of the gradient products)
 #pragma unroll
@@ -683,19 +696,20 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         float z[128];
 #pragma unroll
         for (int i = 0; i < 128; ++i) z[i] = 0.f;
-        for (int kc = t.kc0; kc < t.kc1; kc += SEG, ++tl) add_segment(tl, z);
+        for (int kc = t.kc0; kc < t.kc1 && !timed_out; kc += SEG, ++tl) add_segment(tl, z);
+        if (timed_out) break;
         if constexpr (EPI == kGather) gather_finish(ea, tmO, sh, z);
         else fwd_finish(ea, sh, z);
         if constexpr (EPI == kFwdKeep) f32_finish<EPI>(ea, tmO, sh, z);
       } else {
         const int b = tl & 1;
-        if (!mbar_wait_bounded(accf0 + 8 * b, uint32_t(tl >> 1) & 1u)) timed_out = true;
-        tc::fence_after_sync();
+        if (!arrived(tl)) break;
         // to registers at once, so that the next tile's MMAs have the accumulator early
         float z[128];
         tmem_ld128(tmem_base + lanes + uint32_t(b * 256 + sh.c0), z);
         release(b);
-        for (int kc = t.kc0 + SEG; kc < t.kc1; kc += SEG) add_segment(++tl, z);
+        for (int kc = t.kc0 + SEG; kc < t.kc1 && !timed_out; kc += SEG) add_segment(++tl, z);
+        if (timed_out) break;
         if constexpr (EPI == kDz) dz_finish(ea, tmO, sh, z);
         else if constexpr (EPI == kDwBf16) bf16_finish(ea, tmO, sh, z);
         else f32_finish<EPI>(ea, tmO, sh, z);
@@ -707,8 +721,14 @@ product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   if (timed_out) atomicOr(&ea.ws.hdr->status, kFlagTimeout);
   if (wk.beside) pdl_wait();
   tc::fence_before_sync();
-  if constexpr (CG == 1) __syncthreads();
-  else cluster_sync();  // the pair's barriers and TMEM stay until both are done
+  // A role whose wait has run out leaves its loop, and the roles that wait for it run out in
+  // turn.  What they have in flight (copies into shared memory, MMAs) waits for nobody and
+  // lands in microseconds: it gets a millisecond before memory and TMEM are given back.
+  if (__syncthreads_or(timed_out)) {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < kDrainNs) {}
+  }
+  if constexpr (CG == 2) cluster_sync();  // the pair's barriers and TMEM stay until both are done
   tc::fence_after_sync();
   if (warp == 1) {
     if constexpr (CG == 1) tc::tmem_dealloc(tmem_base, 512);
