@@ -339,9 +339,10 @@ DSPARK_API dspark_status_t dspark_tp_heads_bwd(const dspark_problem_t* prob, con
  * over the whole vocabulary, from the hidden rows and the head, with its gradients.  The
  * caller has no logits: the forward leaves one logsumexp per row, the backward forms dL/dz
  * again, one piece of the vocabulary at a time.  Only where all the FP32 logits take at most
- * 320 MiB, and the forward's ws_bytes has room for a backward, do they stay there and spare
- * the backward a product; the workspace says which, and a backward goes by that.  (The CE
- * term of dspark_loss_fwd, for callers that have hidden rows instead of logits.)
+ * 320 MiB, that is faster (not with small hidden sizes), and the forward's ws_bytes has room
+ * for a backward, do they stay there and spare the backward a product; the workspace says
+ * which, and a backward goes by that.  (The CE term of dspark_loss_fwd, for callers that have
+ * hidden rows instead of logits.)
  *   lse_r = logsumexp(z_r),   CE_r = lse_r - z_r[target_r]
  *   loss  = sum_r w_r * (CE_r + z_alpha * lse_r^2)          (unnormalised numerator)
  *   dz_r  = g * w_r * (softmax(z_r) * (1 + 2 z_alpha lse_r) - onehot(target_r))
@@ -397,8 +398,8 @@ typedef struct {
 /* Bytes of device workspace for `prob`: for the forward alone (grads NULL), or for the
  * forward and the backward with these gradients.  0 on an invalid problem.  Depends on the
  * sizes and on which gradients are non-NULL.  With gradients it holds a piece of dL/dz of
- * about 256 MiB at most (never less than 256 columns of it), and the FP32 logits where they
- * take at most 320 MiB. */
+ * about 256 MiB at most (never less than 256 columns of it), and room for the FP32 logits
+ * where they take at most 320 MiB. */
 DSPARK_API size_t dspark_lce_workspace_size(const dspark_lce_problem_t* prob, const dspark_lce_grads_t* grads);
 
 /* Forward.  `ws` 256-byte aligned, dspark_lce_workspace_size(prob, NULL) bytes, or as many

@@ -15,9 +15,20 @@ constexpr size_t kPieceBytes = size_t(256) << 20;    // bound on the kept piece 
 constexpr int kMaxSplitTiles = 32;                   // more row tiles than this are not split
 constexpr int kMaxSplit = 32;
 constexpr size_t kPlaneBytes = size_t(96) << 20;     // bound on split planes (they stay in L2)
-// The logits of a problem whose FP32 logits take no more than this stay in the workspace for
-// the backward (at 448 rows of 151936 columns 260 MiB), which is then spared a product.
+// A workspace with room for a backward has room for FP32 logits up to this size; where they
+// stay, the backward is spared a product.
 constexpr size_t kKeepBytes = size_t(320) << 20;
+// Whether that pays: the product spared grows with the hidden size, the traffic added does not,
+// and logits that stay in L2 cost little.  Both gradients, kept against formed again, us:
+//   24 MiB, H 64 (41 x 151936)      89 /  93     140 MiB, H 640 (1146 x 32003)   236 /  236
+//   63 MiB, H 64 (524 x 32003)      93 /  93     140 MiB, H 768 (241 x 151936)   299 /  308
+//   96 MiB, H 256 (165 x 151936)   162 / 152     300 MiB, H 64 (517 x 151936)    310 /  254
+//   96 MiB, H 512 (786 x 32003)    146 / 149     300 MiB, H 640 (2457 x 32003)   452 /  439
+//  140 MiB, H 512 (1146 x 32003)   193 / 184     300 MiB, H 768 (517 x 151936)   596 /  619
+//                                                260 MiB, H 4096 (448 x 151936) 1826 / 2247
+inline bool keep_pays(size_t bytes, int64_t H) {
+  return bytes <= size_t(40) << 20 || (bytes <= size_t(100) << 20 && H >= 512) || H > 640;
+}
 // A gathered forward takes the reference of a row's exponentials from this many columns.
 constexpr int kSampleCols = 2048;
 // A logit more than this many octaves above a row's reference sends the call the other way.
@@ -48,7 +59,8 @@ struct Plan {
   int64_t plane_rows;  // rows of the hidden gradient's partial sums, all planes together
   uint8_t ksplit[kMaxSplitTiles + 1];  // its K splits (planes) by the number of row tiles
   int64_t merge_blocks;
-  int keep;            // the logits stay in the workspace if the forward was given room for a backward
+  int room;            // a backward's workspace has room for the logits
+  int keep;            // they stay there if the forward was given that room
   int gathered;        // the forward also gathers the hidden gradient (no head gradient follows)
 };
 
@@ -100,7 +112,8 @@ inline Plan make_plan(int64_t R, int64_t V, int64_t H, bool hidden_grad_only) {
   }
   p.merge_blocks = ceil_div(R, kMergeRows);
   p.gathered = hidden_grad_only && V >= kGatherFrom;
-  p.keep = !p.gathered && p.pieces == 1 && 4 * size_t(p.Rp) * size_t(p.piece) <= kKeepBytes;
+  p.room = !p.gathered && p.pieces == 1 && 4 * size_t(p.Rp) * size_t(p.piece) <= kKeepBytes;
+  p.keep = p.room && keep_pays(4 * size_t(R) * size_t(V), H);
   return p;
 }
 
@@ -129,7 +142,7 @@ inline Offsets offsets(const Plan& p, bool bwd, bool dhidden) {
   take(o.ref, 4 * R);
   take(o.hsup, 2 * Rp * size_t(p.H));
   take(o.part, sizeof(float2) * 2 * size_t(p.fwd_tiles) * Rp);
-  take(o.z, bwd && p.keep ? 4 * Rp * size_t(p.piece) : 0);
+  take(o.z, bwd && p.room ? 4 * Rp * size_t(p.piece) : 0);
   take(o.dz, bwd ? 2 * Rp * size_t(p.piece) : 0);
   take(o.planes, bwd && dhidden ? sizeof(float) * size_t(p.plane_rows) * size_t(p.H) : 0);
   o.bytes = off;

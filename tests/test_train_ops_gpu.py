@@ -928,3 +928,18 @@ def test_clip_refuses_tensors_that_share_memory(T):
                         ([a], [buf[8:48]])):
         with pytest.raises(ValueError, match="overlap|listed twice"):
             T.GradClip(grads, 1.0, outs=outs)
+
+
+@pytest.mark.parametrize("R,V,H,kept", [(64, 151936, 64, True), (80, 151936, 64, False), (160, 151936, 448, False),
+                                        (160, 151936, 512, True), (200, 151936, 640, False),
+                                        (200, 151936, 704, True), (600, 151936, 704, False)])
+def test_linear_ce_keeps_logits_where_that_is_faster(T, R, V, H, kept):
+    """By the logits' size and the hidden size; the results hold either way."""
+    h, w, t, a = lce_inputs(R, V, H, 7, seed=36)
+    call = T.LinearCE(h, w, t, row_weight=a)
+    call.forward()
+    call.backward()
+    assert call.check_status() == 0
+    head = call.ws[call.ws_ptr.value - call.ws.data_ptr():][:32].view(torch.int32).tolist()
+    assert head[1] == R - 7 and head[4] == kept  # the workspace's header: labelled rows, logits kept
+    lce_compare(call, O.linear_ce(h, w, t, a), H, V)
