@@ -356,7 +356,7 @@ DSPARK_API dspark_status_t dspark_tp_heads_bwd(const dspark_problem_t* prob, con
  * gradient products (they run on the bf16 tensor cores), whose FP32 sums are rounded once
  * to the output type.  Two runs give the same bits.
  * H, the leading dimensions and every matrix pointer obey the 16-byte rule above; V and R
- * are free.  Sizes above 2^30 columns, 2^24 rows, a hidden size above 2^20 or more than
+ * are free, from 1 on (an empty batch is DSPARK_ERR_INVALID_ARG).  Sizes above 2^30 columns, 2^24 rows, a hidden size above 2^20 or more than
  * 2^31 - 1 tiles (R/128 x V/128) are DSPARK_ERR_UNSUPPORTED.
  */
 typedef struct {
@@ -431,7 +431,8 @@ DSPARK_API dspark_status_t dspark_lce_bwd(const dspark_lce_problem_t* prob, cons
  * give the same bits.
  *
  * `dtype` is the type of table and out, or of dout.  D, the leading dimensions and the
- * matrix pointers obey the 16-byte rule above; Vt and R are free.  More than 2^24 rows,
+ * matrix pointers obey the 16-byte rule above; Vt and R are free, from 1 on (an empty batch is
+ * DSPARK_ERR_INVALID_ARG: its gradient is a zero table).  More than 2^24 rows,
  * 2^30 table rows or 2^20 columns are DSPARK_ERR_UNSUPPORTED.
  */
 typedef struct {

@@ -545,6 +545,8 @@ class _EmbedCall(_DeviceCall):
         _need(valid, torch.uint8, "valid")
         if ids.numel() != R or (valid is not None and valid.numel() != R):
             raise ValueError(f"ids and valid must hold {R} values")
+        if R < 1:
+            raise ValueError("ids must hold at least one value")
         self.device = ids.device
         _same_device(self.device, valid=valid)
         p = abi.dspark_embed_problem_t()
@@ -625,21 +627,33 @@ class GradClip(_DeviceCall):
             raise ValueError("grads must hold at least one tensor, and outs as many")
         self.device = grads[0].device
         arr = (abi.dspark_tensor_t * len(grads))()
-        seen = set()
+        seen, spans = set(), []  # spans: what is read, and what is written elsewhere
         for i, (g, o) in enumerate(zip(grads, outs)):
-            if g.dtype not in _ABI_DTYPE or o.dtype != g.dtype or o.numel() != g.numel():
+            dtype = g.dtype
+            if dtype not in _ABI_DTYPE or o.dtype != dtype or o.numel() != g.numel():
                 raise ValueError(f"grads[{i}] must be bf16 or fp32, and outs[{i}] like it")
-            _need(g, g.dtype, f"grads[{i}]")
-            _need(o, g.dtype, f"outs[{i}]")
-            _same_device(self.device, **{f"grads[{i}]": g, f"outs[{i}]": o})
-            if g.numel() and g.data_ptr() in seen:
-                raise ValueError(f"grads[{i}] is listed twice")
-            seen.add(g.data_ptr())
-            arr[i] = abi.dspark_tensor_t(g.data_ptr(), o.data_ptr(), g.numel(), _ABI_DTYPE[g.dtype])
-        # what is read and what is written elsewhere: no two of them may share memory
-        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
-                       for t in grads + [o for g, o in zip(grads, outs) if o.data_ptr() != g.data_ptr()] if t.numel())
-        if any(end > start for (_, end), (start, _) in zip(spans, spans[1:])):
+            _need(g, dtype, f"grads[{i}]")
+            if g.device != self.device:
+                _same_device(self.device, **{f"grads[{i}]": g})
+            n, src = g.numel(), g.data_ptr()
+            dst = src
+            if o is not g:
+                _need(o, dtype, f"outs[{i}]")
+                if o.device != self.device:
+                    _same_device(self.device, **{f"outs[{i}]": o})
+                dst = o.data_ptr()
+            if n:
+                if src in seen:
+                    raise ValueError(f"grads[{i}] is listed twice")
+                seen.add(src)
+                nbytes = n * g.element_size()
+                spans.append((src, src + nbytes))
+                if dst != src:
+                    spans.append((dst, dst + nbytes))
+            t = arr[i]
+            t.src, t.dst, t.n, t.dtype = src, dst, n, _ABI_DTYPE[dtype]
+        spans.sort()
+        if any(spans[i][1] > spans[i + 1][0] for i in range(len(spans) - 1)):
             raise ValueError("grads and outs must not overlap (outs[i] may be grads[i])")
         self.tensors, self.count, self.max_norm, self.group = arr, len(grads), float(max_norm), group
         self.grads, self.outs = grads, outs

@@ -943,3 +943,20 @@ def test_linear_ce_keeps_logits_where_that_is_faster(T, R, V, H, kept):
     head = call.ws[call.ws_ptr.value - call.ws.data_ptr():][:32].view(torch.int32).tolist()
     assert head[1] == R - 7 and head[4] == kept  # the workspace's header: labelled rows, logits kept
     lce_compare(call, O.linear_ce(h, w, t, a), H, V)
+
+
+def test_empty_batches_are_refused(T):
+    """No rows: refused by name before anything is launched; empty tensors among others to clip
+    are not (also where they lie at another's first element)."""
+    none = torch.empty(0, dtype=torch.int64, device="cuda")
+    table = torch.zeros(5, 8, device="cuda")
+    with pytest.raises(ValueError, match="at least one"):
+        T.Embedding(none, table)
+    with pytest.raises(ValueError, match="at least one"):
+        T.EmbeddingGrad(none, table[:0], 5)
+    with pytest.raises(ValueError, match="at least one"):
+        T.LinearCE(table[:0].to(torch.bfloat16), table.to(torch.bfloat16), none)
+    buf = torch.ones(64, device="cuda")
+    call = T.GradClip([buf[:0], buf, buf[64:]], 1.0)
+    call.launch()
+    assert abs(float(call.norm) - 8.0) <= 2.0 ** -20
