@@ -427,20 +427,33 @@ _ABI_DTYPE = {torch.float32: abi.DSPARK_F32, torch.bfloat16: abi.DSPARK_BF16}
 
 class _DeviceCall:
     """What the prepared calls below share: a workspace, and launches on the current stream
-    of the device that holds the tensors, whichever device is current."""
+    of the device that holds the tensors, whichever device is current.  What a call has
+    allocated is not reused before its launches on any stream are done, also when the call
+    is dropped right behind them."""
 
-    def _workspace(self, nbytes: int) -> None:
+    def _workspace(self, nbytes: int, *allocated) -> None:
+        """The workspace; ``allocated``: what else this call may have allocated itself."""
         if nbytes == 0:
             raise abi.DSparkError(abi.DSPARK_ERR_UNSUPPORTED, type(self).__name__)
         self.ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=self.device)
         self.ws_ptr, self.ws_len = _aligned_ws(self.ws)
+        self._allocated = [self.ws] + [t for t in allocated if t is not None]
+        self._streams = {torch._C._cuda_getCurrentRawStream(self.device.index)}  # that the allocator knows of
+
+    def _used_on(self, s: int) -> None:
+        stream = torch.cuda.ExternalStream(s, device=self.device) if s else torch.cuda.default_stream(self.device)
+        for t in self._allocated:
+            t.record_stream(stream)
+        self._streams.add(s)
 
     def _run(self, fn, where, stream, *args) -> None:
         index = self.device.index
         if torch.cuda.current_device() != index:
             with torch.cuda.device(self.device):
                 return self._run(fn, where, stream, *args)
-        s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream
+        s = torch._C._cuda_getCurrentRawStream(index) if stream is None else int(getattr(stream, "value", stream) or 0)
+        if s not in self._streams:
+            self._used_on(s)
         status = fn(*args, s)
         if status:
             abi.check(status, where)
@@ -521,7 +534,8 @@ class LinearCE(_DeviceCall):
         o.ce_rows, o.lse_rows = _ptr(self.ce_rows), _ptr(self.lse_rows)
         self.out = o
         grads = ctypes.byref(self.grads) if self.grads is not None else None
-        self._workspace(int(abi.dspark_lce_workspace_size(ctypes.byref(p), grads)))
+        self._workspace(int(abi.dspark_lce_workspace_size(ctypes.byref(p), grads)), self.loss_num, self.num_tokens,
+                        self.ce_rows, self.lse_rows, self.grad_scale, self.dhidden, self.dweight)
         self._ran = False
         self._fwd_args = (ctypes.byref(p), ctypes.byref(o), self.ws_ptr, self.ws_len)
         self._bwd_args = (ctypes.byref(p), grads, self.ws_ptr, self.ws_len)
@@ -571,7 +585,7 @@ class Embedding(_EmbedCall):
             raise ValueError(f"out must be [{R}, {D}]")
         _same_device(self.device, table=table, out=self.out)
         self._keep = (ids, valid, table)
-        self._workspace(int(abi.dspark_embed_workspace_size(ctypes.byref(self.prob), 0)))
+        self._workspace(int(abi.dspark_embed_workspace_size(ctypes.byref(self.prob), 0)), self.out)
         self._args = (ctypes.byref(self.prob), _ptr(table), self.table_ld, _ptr(self.out), out_ld, self.ws_ptr,
                       self.ws_len)
 
@@ -599,7 +613,7 @@ class EmbeddingGrad(_EmbedCall):
             raise ValueError(f"out must be [{vocab}, {D}]")
         _same_device(self.device, dout=dout, out=out)
         self._keep = (ids, valid, dout)
-        self._workspace(int(abi.dspark_embed_workspace_size(ctypes.byref(self.prob), 1)))
+        self._workspace(int(abi.dspark_embed_workspace_size(ctypes.byref(self.prob), 1)), self.out)
         self._args = (ctypes.byref(self.prob), _ptr(dout), dout_ld, _ptr(out), out_ld, _ABI_DTYPE[out.dtype],
                       1 if accumulate else 0, self.ws_ptr, self.ws_len)
 
@@ -671,7 +685,7 @@ class GradClip(_DeviceCall):
         self.norm = torch.zeros(1, dtype=torch.float32, device=self.device)
         self.coef = torch.ones(1, dtype=torch.float32, device=self.device)
         self.sumsq = torch.zeros(1, dtype=torch.float64, device=self.device)
-        self._workspace(int(abi.dspark_grad_workspace_size(self.count)))
+        self._workspace(int(abi.dspark_grad_workspace_size(self.count)), self.norm, self.coef, self.sumsq)
         self._tail = (self.max_norm, _ptr(self.norm), _ptr(self.coef), self.ws_ptr, self.ws_len)
 
     def launch(self, stream=None) -> None:

@@ -960,3 +960,35 @@ def test_empty_batches_are_refused(T):
     call = T.GradClip([buf[:0], buf, buf[64:]], 1.0)
     call.launch()
     assert abs(float(call.norm) - 8.0) <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_what_a_dropped_call_allocated_waits_for_its_stream(T, given):
+    """A call built on one stream, launched on another behind other work there and dropped:
+    its memory goes to nobody before that launch is done."""
+    h, w, t, a = lce_inputs(300, 5000, 256, 9, seed=37)
+    ids = torch.randint(0, 700, (300,), device="cuda")
+    g = torch.randn(100000, device="cuda")
+    out = torch.empty_like(g)
+    made = [lambda: T.LinearCE(h, w, t, row_weight=a, dhidden=False, dweight=False),
+            lambda: T.EmbeddingGrad(ids, h, 700, dtype=torch.bfloat16), lambda: T.Embedding(ids, w),
+            lambda: T.GradClip([g], 1.0, outs=[out])]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # a tenth of a second of waiting
+    for make in made:
+        call = make()
+        run = call.forward if isinstance(call, T.LinearCE) else call.launch
+        if given:
+            run(stream=side.cuda_stream)
+        else:
+            with torch.cuda.stream(side):
+                run()
+        held = {x.data_ptr(): x.numel() * x.element_size() for x in (call.ws, getattr(call, "out", None),
+                                                                    getattr(call, "norm", None)) if isinstance(x, torch.Tensor)}
+        assert not side.query()
+        del call, run
+        again = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in held.values() for _ in range(3)]
+        assert not side.query() and not held.keys() & {x.data_ptr() for x in again}
+    torch.cuda.synchronize()
