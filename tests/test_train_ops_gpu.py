@@ -974,9 +974,13 @@ def test_what_a_dropped_call_allocated_waits_for_its_stream(T, given):
             lambda: T.EmbeddingGrad(ids, h, 700, dtype=torch.bfloat16), lambda: T.Embedding(ids, w),
             lambda: T.GradClip([g], 1.0, outs=[out])]
     side = torch.cuda.Stream()
-    torch.cuda.synchronize()
+    for make in made:  # once before, so that nothing below has to load code first
+        call = make()
+        (call.forward if isinstance(call, T.LinearCE) else call.launch)(stream=side.cuda_stream if given else None)
+        torch.cuda.synchronize()
+        del call
     with torch.cuda.stream(side):
-        torch.cuda._sleep(200_000_000)  # a tenth of a second of waiting
+        torch.cuda._sleep(1_000_000_000)  # half a second of waiting
     for make in made:
         call = make()
         run = call.forward if isinstance(call, T.LinearCE) else call.launch
