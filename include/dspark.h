@@ -399,7 +399,10 @@ typedef struct {
  * forward and the backward with these gradients.  0 on an invalid problem.  Depends on the
  * sizes and on which gradients are non-NULL.  With gradients it holds a piece of dL/dz of
  * about 256 MiB at most (never less than 256 columns of it), and room for the FP32 logits
- * where they take at most 320 MiB. */
+ * where they take at most 320 MiB.  The forward's own largest parts are the rows'
+ * statistics, 8 bytes for each row and 128 columns (R V / 16 bytes: 74 MiB at 8192 rows of
+ * 151936 columns, where bf16 logits would take 2.3 GiB), and a copy of the labelled hidden
+ * rows. */
 DSPARK_API size_t dspark_lce_workspace_size(const dspark_lce_problem_t* prob, const dspark_lce_grads_t* grads);
 
 /* Forward.  `ws` 256-byte aligned, dspark_lce_workspace_size(prob, NULL) bytes, or as many
@@ -420,15 +423,18 @@ DSPARK_API dspark_status_t dspark_lce_bwd(const dspark_lce_problem_t* prob, cons
 /*
  * Scaled embedding lookup and its gradient (the gather that feeds a drafter, and the table
  * gradient dW1 of dspark_grads_t in a form whose sums have a fixed order).
- *   out_r    = scale * table[id_r]                       (rounded once to the table's type)
- *   dtable_i = scale * sum over rows r with id_r = i of dout_r, added in row order in FP32
+ *   out_r    = scale * table[id_r]       (the product in FP32, rounded to the table's type)
+ *   dtable_i = scale * sum over rows r with id_r = i of dout_r, added in FP32
  * A row whose `valid` is 0 gives a zero output row and no gradient; its id is not looked at.
  * An id outside [0, Vt) raises DSPARK_ERR_ID_OUT_OF_RANGE and counts as not valid.
  *
  * dspark_embed_bwd sorts the rows by id (a stable radix sort on the device), sums each id's
  * rows and writes each touched table row once.  Without `accumulate` every other row is
- * zeroed; with it the sums are added and other rows are neither read nor written.  Two runs
- * give the same bits.
+ * zeroed; with it the sums are added and other rows are neither read nor written.
+ * The additions have a fixed order for given sizes and ids: an id's rows are taken in row
+ * order, as they fall into windows of consecutive sorted rows, and the windows' sums are added
+ * in window order.  Two runs give the same bits; where the windows end depends on R, D, the
+ * type and the other rows' ids, so the same rows among others may differ in rounding.
  *
  * `dtype` is the type of table and out, or of dout.  D, the leading dimensions and the
  * matrix pointers obey the 16-byte rule above; Vt and R are free, from 1 on (an empty batch is

@@ -4,8 +4,9 @@
 // The gradient sorts (id, row) by id with a stable radix sort, so an id's rows come in row
 // order, then sums windows of consecutive sorted rows.  A segment (the rows of one id) that
 // lies inside a window is finished there; one that crosses a window's end leaves a partial
-// sum, and the partial sums of a segment are added in window order.  Every sum has a fixed
-// order whatever runs when: no floating-point atomics.
+// sum, and the partial sums of a segment are added in window order.  Every sum has an order
+// that the sizes and the ids fix, whatever runs when.  The one floating-point atomic is the
+// addition to an accumulated table, one per element and call.
 #include <cuda_bf16.h>
 
 #include <algorithm>

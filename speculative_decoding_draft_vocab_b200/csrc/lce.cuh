@@ -1,5 +1,5 @@
-// Linear cross entropy (softmax cross entropy of hidden . weight^T, logits never kept):
-// the plan a shape gets, its workspace map and the launchers.
+// Linear cross entropy (softmax cross entropy of hidden . weight^T): the plan a shape gets,
+// its workspace map and the launchers.
 #pragma once
 #include "internal.cuh"
 
@@ -29,11 +29,25 @@ constexpr size_t kKeepBytes = size_t(320) << 20;
 inline bool keep_pays(size_t bytes, int64_t H) {
   return bytes <= size_t(40) << 20 || (bytes <= size_t(100) << 20 && H >= 512) || H > 640;
 }
-// A gathered forward takes the reference of a row's exponentials from this many columns.
+// A gathered forward takes the reference of a row's exponentials from this many columns (1024,
+// 2048, 4096 of 32003, 1600 rows of 1000: 276, 278, 285 us; fewer leave rows out of range
+// sooner).
 constexpr int kSampleCols = 2048;
 // A logit more than this many octaves above a row's reference sends the call the other way.
 constexpr float kGatherRange = 96.f;
-// From this vocabulary on it pays: it saves one of three products and adds the sample.
+// It saves one of three products and adds the sample and kernels that mostly return at once.
+// Against forming the logits again it pays from this vocabulary on, but for few rows of a small
+// hidden size; where logits of at most about 100 MiB could have been kept instead (which this
+// rule does not look at) that was faster still.  Hidden gradient alone, gathered / kept /
+// formed again, us:
+//   rows x columns x H     448 x   8192 x 4096   128 /   90 /  116   (forced)
+//                          448 x  16384 x 4096   190 /  157 /  213
+//                         4096 x  16384 x 4096  1005 / 1044 / 1348
+//                           56 x  32003 x 1000    80 /   61 /   71
+//                         1600 x  32003 x 1000   282 /  322 /  358
+//                           56 x 151936 x 4096   498 /  472 /  675
+//                          448 x 151936 x  512   224 /  292 /  269
+//                         1600 x 151936 x 4096  3760 /    - / 5182
 constexpr int64_t kGatherFrom = 16384;
 constexpr int kMergeRows = 32;                       // rows per CTA of the merge kernel
 

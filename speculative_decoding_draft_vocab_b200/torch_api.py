@@ -466,8 +466,9 @@ class _DeviceCall:
 
 class LinearCE(_DeviceCall):
     """A prepared linear cross entropy: the loss of ``hidden @ weight.T`` against
-    ``targets`` over the whole vocabulary and its gradients, in a workspace that does not grow
-    with the logits (dspark_lce_fwd, dspark_lce_bwd).
+    ``targets`` over the whole vocabulary and its gradients, without the logits but where
+    they are few (dspark_lce_fwd, dspark_lce_bwd).  The workspace holds at most about 256 MiB
+    of their gradient, 320 MiB of FP32 logits and R V / 16 bytes of row statistics.
 
     ``hidden`` [R, H] and ``weight`` [V, H] are bf16 with contiguous rows, ``targets`` [R]
     int64, ``row_weight`` [R] fp32.  forward() writes ``loss_num``, ``num_tokens``,
@@ -595,8 +596,8 @@ class Embedding(_EmbedCall):
 
 class EmbeddingGrad(_EmbedCall):
     """A prepared table gradient (dspark_embed_bwd): ``out[i] = scale * sum of the rows of
-    dout whose id is i``, in row order, every other row zero; with ``accumulate`` (fp32)
-    added to ``out``.  ``dout`` [ids.numel(), D] is bf16 or fp32 with contiguous rows;
+    dout whose id is i``, in a fixed order of additions, every other row zero; with
+    ``accumulate`` (fp32) added to ``out``.  ``dout`` [ids.numel(), D] is bf16 or fp32 with contiguous rows;
     ``out`` [vocab, D] of type ``dtype`` is allocated unless given."""
 
     def __init__(self, ids: torch.Tensor, dout: torch.Tensor, vocab: int, scale: float = 1.0,
