@@ -996,3 +996,85 @@ def test_what_a_dropped_call_allocated_waits_for_its_stream(T, given):
         again = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in held.values() for _ in range(3)]
         assert not side.query() and not held.keys() & {x.data_ptr() for x in again}
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------- offsets that 32 bits do not hold
+def test_embedding_past_32_bits(T):
+    """A table of 2.46e9 elements: rows at its end, looked up and given gradients."""
+    Vt, D, R = 600001, 4096, 700
+    g = torch.Generator(device="cuda").manual_seed(50)
+    ids = torch.randint(0, Vt, (R,), generator=g, device="cuda")
+    ids[:3] = torch.tensor([Vt - 1, Vt - 2, 524288], device="cuda")  # (524288 x 4096 = 2^31)
+    table = torch.zeros(Vt, D, dtype=torch.bfloat16, device="cuda")
+    table[ids] = torch.randn(R, D, generator=g, device="cuda").to(torch.bfloat16)
+    look = T.Embedding(ids, table, scale=2.0)
+    look.launch()
+    assert look.check_status() == 0 and torch.equal(look.out, table[ids] * 2)
+    grad = T.EmbeddingGrad(ids, look.out, Vt, out=table.fill_(7.0))
+    grad.launch()
+    assert grad.check_status() == 0
+    touched, where = torch.unique(ids, return_inverse=True)
+    want = torch.zeros(touched.numel(), D, dtype=torch.float64, device="cuda").index_add_(0, where, look.out.double())
+    mag = torch.zeros_like(want).index_add_(0, where, look.out.double().abs())
+    n = torch.bincount(where)[:, None]
+    assert bool(((table[touched].double() - want).abs() <= 1.01 * ((n + 2) * U32 * mag + U16 * want.abs())).all())
+    table[touched] = 0
+    assert not bool(table.any())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_clip_past_32_bits(T, dtype):
+    n = (1 << 31) + 12345
+    g = torch.full((n,), 0.5, dtype=dtype, device="cuda")
+    g[::4097] = -2.0
+    more = n // 4097 + 1
+    norm = (0.25 * (n - more) + 4.0 * more) ** 0.5
+    call = T.GradClip([g, torch.zeros(3, device="cuda")], norm / 2)
+    call.launch()
+    assert call.check_status() == 0
+    # FP64 sums of squares each right to 2^-22, one square root and three FP32 roundings
+    assert abs(float(call.norm) - norm) <= 2.0 ** -21 * norm
+    coef = norm / 2 / (norm + 1e-6)
+    tol = (2.0 ** -20 + 1.01 * _u(dtype)) * coef
+    assert float((g[::4097].double() + 2.0 * coef).abs().max()) <= 2.0 * tol
+    g[::4097] = g[1]
+    assert bool((g == g[1]).all()) and abs(float(g[1]) - 0.5 * coef) <= 0.5 * tol
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_linear_ce_past_32_bits(T, dtype):
+    """A head of 2.46e9 elements; its gradient compared in the rows of labels, around the
+    places that 31 and 32 bits of elements and bytes end at, and at the end."""
+    R, V, H = 70, 300001, 8192
+    h, w, t, a = lce_inputs(R, V, H, 4, seed=51)
+    t[:2] = torch.tensor([V - 1, 262144], device="cuda")
+    call = T.LinearCE(h, w, t, row_weight=a, dweight_dtype=dtype)
+    call.forward()
+    call.backward()
+    assert call.check_status() == 0
+    live = t != -100
+    hd, td = h[live].double(), t[live]
+    z = torch.cat([hd @ p.double().T for p in w.split(20000)], dim=1)
+    lse = torch.logsumexp(z, dim=1)
+    reach = float(max((h[live].float().abs() @ p.float().abs().T).max() for p in w.split(20000)))
+    E = (32 + H / 512 + 2) * 2.0 ** -23 * reach
+    assert bool(((call.lse_rows[live].double() - lse).abs() <= E + 2.0 ** -20 + 2.0 ** -22 * lse.abs()).all())
+    ad = a[live].double()[:, None]
+    p = torch.exp(z - lse[:, None]) * ad
+    dz = p.clone()
+    dz[torch.arange(td.numel(), device="cuda"), td] -= ad[:, 0]
+    P = 2 * ((H / 16 + 2) * 2.0 ** -23 * reach + E) + 2.0 ** -20
+    rows = torch.cat([td, torch.arange(0, V, 9973, device="cuda"), torch.arange(131070, 131075, device="cuda"),
+                      torch.arange(262142, 262147, device="cuda"), torch.arange(V - 300, V, device="cuda")])
+    want, mag = dz[:, rows].T @ hd, dz[:, rows].abs().T @ hd.abs()
+    tol = P * (p[:, rows].T @ hd.abs()) + (U16 + (R / 16 + 2) * 2.0 ** -23) * mag + _u(dtype) * want.abs()
+    assert bool(((call.dweight[rows].double() - want).abs() <= tol * 1.01).all())
+    dh = mag = pmag = 0
+    for v0 in range(0, V, 20000):
+        part = w[v0:v0 + 20000].double()
+        dh = dh + dz[:, v0:v0 + 20000] @ part
+        mag = mag + dz[:, v0:v0 + 20000].abs() @ part.abs()
+        pmag = pmag + p[:, v0:v0 + 20000] @ part.abs()
+    tol = P * pmag + (U16 + (V / 16 + 2) * 2.0 ** -23) * mag + U16 * dh.abs()
+    assert bool(((call.dhidden[live].double() - dh).abs() <= tol * 1.01).all())
+    assert not bool(call.dhidden[~live].any())
